@@ -12,14 +12,16 @@ Two layers:
   ``gdn2_get_device_status``: the C entry points of ``include/gdn2.h`` under
   the same names, taking torch tensors (or None) where the C call takes
   pointers, and raising ``Gdn2Error`` on a non-zero status.
-* ``forward``, ``backward``, ``decode_step``: allocate outputs and workspace
-  with torch (device memory is PyTorch's job here) and call the above on the
+* ``forward``, ``backward``, ``decode_step``, and on a paged key-value cache
+  (``PagedKV``) ``kv_append``, ``attn_decode_step``, ``kv_evict``: allocate
+  outputs and workspace with torch (device memory is PyTorch's job here) and call the above on the
   current CUDA stream; ``forward`` and ``backward`` then read the device
   status word and raise on a recorded error unless called with check=False.
 """
 
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 from typing import Dict, Optional
@@ -44,6 +46,16 @@ class Gdn2Error(RuntimeError):
         self.status = status
         msg = lib().gdn2_status_string(status).decode()
         super().__init__(f"{fn} returned {STATUS.get(status, status)}: {msg}")
+
+
+class _PagedKVStruct(ctypes.Structure):
+    """gdn2_paged_kv of include/gdn2.h."""
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("weight", ctypes.c_void_p),
+                ("block_table", ctypes.c_void_p), ("seq_lens", ctypes.c_void_p),
+                ("stride_page", ctypes.c_longlong), ("stride_slot", ctypes.c_longlong),
+                ("stride_head", ctypes.c_longlong), ("num_pages", ctypes.c_int),
+                ("page_size", ctypes.c_int), ("max_pages", ctypes.c_int), ("N", ctypes.c_int),
+                ("H_kv", ctypes.c_int), ("d", ctypes.c_int), ("io", ctypes.c_int)]
 
 
 _lib: Optional[ctypes.CDLL] = None
@@ -90,6 +102,16 @@ def lib() -> ctypes.CDLL:
         L.gdn2_version.restype = i
         L.gdn2_fwd_noalloc.argtypes = [vp] * 9 + [i] * 7 + [vp]
         L.gdn2_fwd_noalloc.restype = i
+        L.gdn2_kv_append.argtypes = [vp] * 4 + [i, vp, vp]
+        L.gdn2_kv_append.restype = i
+        L.gdn2_attn_decode_workspace_bytes.argtypes = [vp, i, i]
+        L.gdn2_attn_decode_workspace_bytes.restype = sz
+        L.gdn2_attn_decode_step.argtypes = [vp] * 4 + [i, ctypes.c_float, i, i, vp, sz, vp]
+        L.gdn2_attn_decode_step.restype = i
+        L.gdn2_kv_evict_workspace_bytes.argtypes = [vp, i]
+        L.gdn2_kv_evict_workspace_bytes.restype = sz
+        L.gdn2_kv_evict.argtypes = [vp, vp, i, i, i, vp, vp, sz, vp]
+        L.gdn2_kv_evict.restype = i
         L.gdn2_kernel_launches.argtypes = []
         L.gdn2_kernel_launches.restype = ctypes.c_ulonglong
         L.gdn2_set_kernel_timer.argtypes = [i]
@@ -228,6 +250,31 @@ def gdn2_decode_step(q, k, v, g, b, w, S, o, N, H, d_k, d_v, io, stream=None):
     rc = lib().gdn2_decode_step(_ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(b), _ptr(w), _ptr(S),
                                 _ptr(o), N, H, d_k, d_v, io, _stream(stream))
     _check("gdn2_decode_step", rc)
+
+
+def gdn2_kv_append(kv, k, v, cu_seqlens, T, lens_out, stream=None):
+    rc = lib().gdn2_kv_append(kv.ref, _ptr(k), _ptr(v), _ptr(cu_seqlens), T, _ptr(lens_out), _stream(stream))
+    _check("gdn2_kv_append", rc)
+
+
+def gdn2_attn_decode_workspace_bytes(kv, H, add_weights) -> int:
+    return int(lib().gdn2_attn_decode_workspace_bytes(kv.ref, H, int(add_weights)))
+
+
+def gdn2_attn_decode_step(kv, q, o, lse, H, scale, window, add_weights, ws, ws_bytes, stream=None):
+    rc = lib().gdn2_attn_decode_step(kv.ref, _ptr(q), _ptr(o), _ptr(lse), H, scale, window,
+                                     int(add_weights), _ptr(ws), ws_bytes, _stream(stream))
+    _check("gdn2_attn_decode_step", rc)
+
+
+def gdn2_kv_evict_workspace_bytes(kv, budget) -> int:
+    return int(lib().gdn2_kv_evict_workspace_bytes(kv.ref, budget))
+
+
+def gdn2_kv_evict(kv, dst, budget, sink, recent, kept, ws, ws_bytes, stream=None):
+    rc = lib().gdn2_kv_evict(kv.ref, dst.ref if dst is not None else None, budget, sink, recent,
+                             _ptr(kept), _ptr(ws), ws_bytes, _stream(stream))
+    _check("gdn2_kv_evict", rc)
 
 
 def gdn2_get_device_status(stream=None) -> int:
@@ -389,3 +436,151 @@ def decode_step(q, k, v, g, b, w, S, o=None, stream=None, gates: str = "activate
     gdn2_decode_step_ex(q, k, v, g, b, w, S, o, N, H, Hv, dk, dv, _io_of(q), _gate_io_of(g, b, w, gates),
                         stream)
     return o
+
+
+# ------------------------------------------------------- paged key-value cache
+
+def _tensor(name: str, t: torch.Tensor, dtype, shape, device) -> None:
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, the cache on {device}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+
+
+class PagedKV:
+    """A paged key-value cache: the tensors, checked once, and their C descriptor.
+
+    k, v: [num_pages, page_size, H_kv, d], float32 or bfloat16, one stride
+    for both, channels contiguous; any order of the other axes in memory (a
+    [num_pages, H_kv, page_size, d] pool is passed as k.transpose(1, 2)).
+    block_table int32 [N, max_pages]; seq_lens int32 [N]; weights float32
+    [num_pages, H_kv, page_size] or None.  The object holds the tensors, whose
+    contents may change at any time (the table and lengths are read by the
+    kernels); a cache of other tensors is another object."""
+
+    __slots__ = ("k", "v", "block_table", "seq_lens", "weights", "device", "struct", "ref", "_ws_bytes")
+
+    def __init__(self, k, v, block_table, seq_lens, weights=None):
+        if k.dim() != 4 or v.shape != k.shape:
+            raise ValueError(f"k and v must share one shape [num_pages, page_size, H_kv, d], got "
+                             f"{tuple(k.shape)} and {tuple(v.shape)}")
+        io = _io_of(k)
+        if v.dtype != k.dtype or v.device != k.device:
+            raise TypeError("k and v must share one dtype and device")
+        pages, page, H, d = k.shape
+        strides = []
+        for axis in range(3):
+            if k.shape[axis] > 1 and k.stride(axis) != v.stride(axis):
+                raise ValueError("k and v must share their strides")
+            strides.append(k.stride(axis))
+        if d > 1 and (k.stride(3) != 1 or v.stride(3) != 1):
+            raise ValueError("the channels of k and v must be contiguous")
+        if block_table.dim() != 2:
+            raise ValueError("block_table must have shape [N, max_pages]")
+        N, width = block_table.shape
+        _tensor("block_table", block_table, torch.int32, (N, width), k.device)
+        _tensor("seq_lens", seq_lens, torch.int32, (N,), k.device)
+        if weights is not None:
+            _tensor("weights", weights, torch.float32, (pages, H, page), k.device)
+        self.k, self.v, self.block_table, self.seq_lens, self.weights = k, v, block_table, seq_lens, weights
+        self.device = k.device
+        self.struct = _PagedKVStruct(k.data_ptr(), v.data_ptr(),
+                                     weights.data_ptr() if weights is not None else None,
+                                     block_table.data_ptr(), seq_lens.data_ptr(), *strides, pages, page, width,
+                                     N, H, d, io)
+        self.ref = ctypes.byref(self.struct)
+        self._ws_bytes = {}  # workspace sizes, by what they depend on
+
+    def workspace_bytes(self, fn: str, *args) -> int:
+        n = self._ws_bytes.get((fn, args))
+        if n is None:
+            n = globals()[fn](self, *args)
+            if n == 0:
+                raise Gdn2Error(fn, 2)
+            self._ws_bytes[(fn, args)] = n
+        return n
+
+
+def _on_stream(kv: PagedKV, stream):
+    """A context in which the cache's device is current, and `stream` too where
+    one is given, so that what is allocated inside belongs to that stream."""
+    if stream is not None:
+        if stream.device != kv.device:
+            raise ValueError(f"the stream is on {stream.device}, the cache on {kv.device}")
+        return torch.cuda.stream(stream)
+    if torch.cuda.current_device() != kv.device.index:
+        return torch.cuda.device(kv.device)
+    return _HERE
+
+
+_HERE = contextlib.nullcontext()
+
+
+def kv_append(kv: PagedKV, k, v, *, cu_seqlens=None, lens_out=None, stream=None) -> None:
+    """Appends k, v [T, H_kv, d] to the cache: one token a sequence (T = N), or
+    packed by cu_seqlens int32 [N+1].  The cache's seq_lens advance, or lens_out
+    [N] takes the new lengths and they stay.  Asynchronous; what the kernels
+    find wrong in the tables is read with check_device_status."""
+    s = kv.struct
+    T = k.shape[0]
+    _tensor("k", k, kv.k.dtype, (T, s.H_kv, s.d), kv.device)
+    _tensor("v", v, kv.k.dtype, (T, s.H_kv, s.d), kv.device)
+    if cu_seqlens is not None:
+        _tensor("cu_seqlens", cu_seqlens, torch.int32, (s.N + 1,), kv.device)
+    if lens_out is None:
+        lens_out = kv.seq_lens
+    else:
+        _tensor("lens_out", lens_out, torch.int32, (s.N,), kv.device)
+    with _on_stream(kv, stream):
+        gdn2_kv_append(kv, k, v, cu_seqlens, T, lens_out)
+
+
+def attn_decode_step(q, kv: PagedKV, *, scale: Optional[float] = None, window: int = 0,
+                     add_weights: bool = False, want_lse: bool = False, o=None, ws=None, stream=None):
+    """Softmax attention of one token for N sequences: q [N,H,d] over each
+    sequence's cached tokens (the last `window` of them if window > 0), query
+    head h reading key-value head h // (H // H_kv).  scale: 1/sqrt(d) unless
+    given.  add_weights=True adds each token's softmax weights to kv.weights.
+    Returns (o [N,H,d], lse float32 [N,H] or None).  Asynchronous, as
+    decode_step."""
+    s = kv.struct
+    if q.dim() != 3:
+        raise ValueError(f"q must have shape [N, H, d], got {tuple(q.shape)}")
+    H = q.shape[1]
+    _tensor("q", q, kv.k.dtype, (s.N, H, s.d), kv.device)
+    with _on_stream(kv, stream):
+        if o is None:
+            o = torch.empty_like(q)
+        else:
+            _tensor("o", o, q.dtype, q.shape, kv.device)
+        lse = torch.empty((s.N, H), dtype=torch.float32, device=kv.device) if want_lse else None
+        if ws is None:
+            ws = torch.empty(kv.workspace_bytes("gdn2_attn_decode_workspace_bytes", H, bool(add_weights)),
+                             dtype=torch.uint8, device=kv.device)
+        gdn2_attn_decode_step(kv, q, o, lse, H, s.d ** -0.5 if scale is None else scale, window,
+                              add_weights, ws, ws.numel())
+    return o, lse
+
+
+def kv_evict(kv: PagedKV, budget: int, *, sink: int = 0, recent: int = 0, dst: Optional[PagedKV] = None,
+             want_kept: bool = False, ws=None, stream=None):
+    """Brings every sequence of more than `budget` tokens back to `budget`: each
+    key-value head keeps its first `sink` and last `recent` tokens and the
+    heaviest of the rest by kv.weights, compacted in order.  In place, or into
+    the cache dst (other pages), which then holds every sequence.  Returns kept
+    int32 [N,H_kv,budget], each slot's former index (-1 behind the end), or None."""
+    s = kv.struct
+    if dst is not None and dst.device != kv.device:
+        raise ValueError(f"dst is on {dst.device}, the cache on {kv.device}")
+    with _on_stream(kv, stream):
+        kept = (torch.empty((s.N, s.H_kv, budget), dtype=torch.int32, device=kv.device)
+                if want_kept and budget > 0 else None)
+        if ws is None:
+            ws = torch.empty(kv.workspace_bytes("gdn2_kv_evict_workspace_bytes", budget) if budget > 0 else 256,
+                             dtype=torch.uint8, device=kv.device)
+        gdn2_kv_evict(kv, dst, budget, sink, recent, kept, ws, ws.numel())
+    return kept

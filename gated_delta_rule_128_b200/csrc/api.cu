@@ -44,7 +44,7 @@ __device__ unsigned int g_status_taken;
 
 // device address of g_status_word in the current device's context, looked up
 // on every call (cheap, allocates nothing, and never stale after a reset)
-static unsigned int *status_word() {
+unsigned int *status_word() {
     void *p = nullptr;
     if (cudaGetSymbolAddress(&p, g_status_word) != cudaSuccess) return nullptr;
     return static_cast<unsigned int *>(p);
@@ -76,7 +76,8 @@ static double g_kind_ms[K_KINDS];
 static const char *const g_kind_names[K_KINDS] = {
     "simt_chunk_prep", "simt_state_fwd", "simt_out_fwd", "simt_state_bwd", "simt_chunk_bwd_a",
     "simt_chunk_bwd_b", "decode_step", "tc_prep", "tc_fwd", "tc_bwd_state", "tc_bwd_grad", "seq_table",
-    "permute_state", "seg_link"};
+    "permute_state", "seg_link", "kv_append", "kv_lens", "attn_split", "attn_join", "evict_select",
+    "evict_move"};
 
 void launch_begin(int kind, cudaStream_t s) {
     g_launches.fetch_add(1, std::memory_order_relaxed);

@@ -1,0 +1,58 @@
+// The paged key-value cache as its kernels see it, and the launchers of the
+// calls on it (gdn2_kv_append, gdn2_attn_decode_step, gdn2_kv_evict).
+#pragma once
+
+#include "common.cuh"
+
+namespace gdn2 {
+
+struct PagedView {
+    char *k, *v;
+    float *w;          // [num_pages, Hkv, page] or nullptr
+    const int *table;  // [N, max_pages]
+    int *lens;         // [N]
+    long long sp, ss, sh;  // strides in bytes; 0 along an axis of extent 1
+    int num_pages, page, page_shift;  // page_shift: log2(page), or -1
+    int max_pages, N, Hkv, d, cap;    // cap = max_pages * page
+    int es;                           // bytes of an element
+};
+
+// token j -> (entry of the sequence's table row, slot in the page)
+__device__ __forceinline__ void page_slot(const PagedView &c, int j, int &entry, int &slot) {
+    if (c.page_shift >= 0) {
+        entry = j >> c.page_shift;
+        slot = j & (c.page - 1);
+    } else {
+        entry = j / c.page;
+        slot = j - entry * c.page;
+    }
+}
+// the page of table entry (n, entry), or -1 where the table names none
+__device__ __forceinline__ int page_of(const PagedView &c, int n, int entry) {
+    const int p = __ldg(c.table + (size_t)n * c.max_pages + entry);
+    return (unsigned)p < (unsigned)c.num_pages ? p : -1;
+}
+__device__ __forceinline__ long long row_off(const PagedView &c, int page, int slot, int h) {
+    return page * c.sp + slot * c.ss + h * c.sh;
+}
+__device__ __forceinline__ size_t weight_off(const PagedView &c, int page, int slot, int h) {
+    return ((size_t)page * c.Hkv + h) * c.page + slot;
+}
+// a sequence's length; 0, with the status recorded, where it is out of range
+__device__ __forceinline__ int checked_len(const PagedView &c, int n, unsigned int *status) {
+    const int len = c.lens[n];
+    if (len >= 0 && len <= c.cap) return len;
+    record_status(status, GDN2_ERR_INVALID_ARG);
+    return 0;
+}
+
+cudaError_t kv_append_launch(const PagedView &c, const void *k, const void *v, const int *cu, int T,
+                             int *lens_out, unsigned int *status, cudaStream_t s);
+size_t attn_ws_bytes(const PagedView &c, int H, int add_weights);
+cudaError_t attn_launch(const PagedView &c, const void *q, void *o, float *lse, int H, float scale,
+                        int window, int add_weights, void *ws, unsigned int *status, cudaStream_t s);
+size_t evict_ws_bytes(const PagedView &c, int budget);
+cudaError_t evict_launch(const PagedView &src, const PagedView &dst, bool in_place, int budget, int sink,
+                         int recent, int *kept, void *ws, unsigned int *status, cudaStream_t s);
+
+}  // namespace gdn2

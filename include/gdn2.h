@@ -227,6 +227,110 @@ gdn2_status gdn2_bwd_varlen(const void *q, const void *k, const void *v, const v
                             const int *cu_seqlens, int N, int T, int H, int H_v, int d_k, int d_v,
                             int chunk, gdn2_io io, gdn2_io gate_io, gdn2_stream_t stream);
 
+/* ------------------------------------------------------------------------
+ * Paged key-value cache and one-token attention.
+ *
+ * The pages describe the mixer both alone and in a hybrid whose other blocks
+ * are softmax attention (LIT-802 review, Table 2; 2K sliding window).  These
+ * calls are the attention blocks' half of decoding: a cache in pages, the
+ * one-token attention that reads it (beside gdn2_decode_step), and eviction
+ * of the tokens that received the least attention.
+ *
+ * Layout: token j of sequence n lies in page block_table[n, j / page_size],
+ * slot j % page_size.  Element (page p, slot s, head h, channel c) of k and of
+ * v is at p * stride_page + s * stride_slot + h * stride_head + c (elements of
+ * the io type; channels contiguous), so [page][slot][head][d],
+ * [page][head][slot][d] and k/v interleaved pools are all strides of one form.
+ * k and v share their strides.  A stride whose extent is 1 is not read; the
+ * others must be positive multiples of 16 bytes under which no two rows
+ * overlap.
+ *   weight : what each cached token received so far, float32
+ *       [num_pages, H_kv, page_size] contiguous, or NULL where no call needs it.
+ *   block_table : device int32 [N, max_pages]; entries behind a sequence's
+ *       last page are not read.  seq_lens : device int32 [N].
+ *   Supported: d in {32, 64, 128}; page_size, max_pages, num_pages, N >= 1;
+ *       max_pages * page_size <= 2^31 - 1 - 1024.  N sequences may be empty.
+ * k and v are 16-byte aligned; weight, block_table and seq_lens 4-byte.
+ * Both tables are read on the device only.  A length outside 0 .. max_pages *
+ * page_size makes the call treat that sequence as empty (and write none of
+ * it), a block_table entry that is needed but outside 0 .. num_pages - 1 makes
+ * it leave that page's tokens out; either records GDN2_ERR_INVALID_ARG in the
+ * device status word.  No access leaves the pools.
+ * Sequences may share pages (a common prompt) in every call that only reads
+ * them; a page that a call writes must belong to one sequence. */
+typedef struct {
+    void *k, *v;
+    float *weight;
+    const int *block_table;
+    int *seq_lens;
+    long long stride_page, stride_slot, stride_head;
+    int num_pages, page_size, max_pages, N, H_kv, d;
+    gdn2_io io;
+} gdn2_paged_kv;
+
+/* Appends tokens: the i-th new token of sequence n becomes token
+ * seq_lens[n] + i.
+ *   k, v : [T, H_kv, d] contiguous, io type, 16-byte aligned.
+ *   cu_seqlens : device int32 [N + 1], as for gdn2_fwd_varlen: sequence n's new
+ *       tokens are rows cu_seqlens[n] .. cu_seqlens[n + 1] - 1 (none is allowed).
+ *       NULL: one token a sequence, T = N.  A table that does not rise from 0 to
+ *       T makes the call append nothing, and records GDN2_ERR_INVALID_ARG.
+ *   T >= 0 (0: nothing is written but lens_out).
+ *   lens_out : int32 [N], the lengths with the new tokens.  kv->seq_lens itself
+ *       advances the cache in place; another buffer leaves it as it is.
+ * The new tokens' weights are set to 0 where kv->weight is given.  A sequence
+ * whose new tokens do not fit max_pages * page_size is left as it is (length
+ * too) and records GDN2_ERR_INVALID_ARG.  Slots behind the new length are left
+ * as they were. */
+gdn2_status gdn2_kv_append(const gdn2_paged_kv *kv, const void *k, const void *v,
+                           const int *cu_seqlens, int T, int *lens_out, gdn2_stream_t stream);
+
+/* Bytes of device workspace (at least 256) that gdn2_attn_decode_step needs for
+ * H query heads on the current device; 0 where the sizes are unsupported. */
+size_t gdn2_attn_decode_workspace_bytes(const gdn2_paged_kv *kv, int H, int add_weights);
+
+/* Softmax attention of one new token a sequence over its cached tokens:
+ *   s_j = scale <q, k_j>, j in [max(0, len - window), len) (window = 0: all),
+ *   o = sum_j e^(s_j - lse) v_j,   lse = log sum_j e^(s_j).
+ * Query head h reads key-value head h / (H / H_kv); H a multiple of H_kv.  The
+ * new token attends to itself once it has been appended.
+ *   q, o : [N, H, d] contiguous, io type.   lse : float32 [N, H], or NULL.
+ *   A sequence without tokens gets o = 0 and lse = -inf.
+ *   add_weights : 1 adds sum over the group's heads of e^(s_j - lse) to the
+ *       weight of each token read (kv->weight must be given).  Where sequences
+ *       share a page, each adds to it, in no fixed order.
+ *   scale : finite.  The cache is only read.
+ * bf16: products on the tensor cores, float32 scores and sums; the softmax
+ * weights are rounded to bf16 for the product with v.  float32: all of it in
+ * float32. */
+gdn2_status gdn2_attn_decode_step(const gdn2_paged_kv *kv, const void *q, void *o, float *lse,
+                                  int H, float scale, int window, int add_weights, void *ws,
+                                  size_t ws_bytes, gdn2_stream_t stream);
+
+/* Bytes of device workspace (at least 256) that gdn2_kv_evict needs; 0 where
+ * the sizes are unsupported. */
+size_t gdn2_kv_evict_workspace_bytes(const gdn2_paged_kv *kv, int budget);
+
+/* Brings every sequence of more than `budget` tokens back to `budget`.  Each
+ * key-value head on its own keeps the first `sink` tokens, the last `recent`
+ * ones, and of those between the budget - sink - recent with the largest
+ * weight (equal weights: the earlier token; NaN counts below everything).
+ * Kept tokens keep their order and move, with their weights, to slots
+ * 0 .. budget - 1.
+ *   dst : NULL: in place; seq_lens is updated, and the pages behind the new
+ *       length are free.  Else another cache of the same N, H_kv, d and io whose
+ *       block_table names pages that no source sequence uses: every sequence
+ *       (also one within the budget) is written there with its new length, and
+ *       kv is left as it is (for pages that sequences share).  dst->weight must
+ *       be given; strides, page_size and max_pages may differ, dst must hold
+ *       min(len, budget) tokens a sequence.
+ *   budget >= 1; sink, recent >= 0; sink + recent <= budget.  kv->weight is
+ *       needed.
+ *   kept : int32 [N, H_kv, budget], each new slot's former index (-1 behind the
+ *       new length), or NULL. */
+gdn2_status gdn2_kv_evict(const gdn2_paged_kv *kv, const gdn2_paged_kv *dst, int budget, int sink,
+                          int recent, int *kept, void *ws, size_t ws_bytes, gdn2_stream_t stream);
+
 /* Bytes of the scratch array behind gdn2_fwd_noalloc (64 MiB). */
 #define GDN2_NOALLOC_SCRATCH_BYTES (64u << 20)
 

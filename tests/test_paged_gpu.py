@@ -1,0 +1,471 @@
+"""The paged-cache kernels against the fp64 oracle on the GPU."""
+
+import numpy as np
+import pytest
+import torch
+
+import gated_delta_rule_128_b200 as gdn
+from gated_delta_rule_128_b200 import workloads
+from _paged import DT, bounds, cache, host, on_gpu
+from oracle import paged
+
+pytestmark = pytest.mark.gpu
+NAN = float("nan")
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    gdn.lib()
+
+
+@pytest.fixture(autouse=True)
+def _status():
+    gdn.gdn2_get_device_status()
+    yield
+    torch.cuda.synchronize()
+
+
+def query(N, H, d, io, seed, mul=1.0):
+    q = (torch.randn(N, H, d, generator=torch.Generator().manual_seed(seed)) * mul).to(DT[io])
+    return q.cuda(), q.double().numpy()
+
+
+def same(a, b):
+    """Equal, NaN equal to NaN."""
+    return np.array_equal(a, b, equal_nan=True)
+
+
+def check(kv, c, q, q64, io, scale, window=0, add=False, status=0):
+    o, lse = gdn.attn_decode_step(q, kv, scale=scale, window=window, add_weights=add, want_lse=True)
+    assert gdn.gdn2_get_device_status() == status
+    w0 = c["w"].copy()
+    r, rl, a, smax = paged.attention(c, q64, scale, window, add)
+    longest = max([paged.length(c, n) for n in range(len(c["lens"]))] + [1])
+    bo, bl, bp = bounds(io, r, rl, a, smax, longest, q64.shape[2])
+    err = np.abs(o.double().cpu().numpy() - r)
+    assert (err <= bo).all(), float((err / bo).max())
+    got = lse.double().cpu().numpy()
+    assert np.array_equal(np.isneginf(got), np.isneginf(rl))
+    fin = np.isfinite(rl)
+    assert (np.abs(got[fin] - rl[fin]) <= bl[fin]).all()
+    if add:
+        w = kv.weights.double().cpu().numpy()
+        fin = np.isfinite(c["w"])
+        added = c["w"] - w0
+        G = q64.shape[1] // c["k"].shape[2]
+        lim = bp.max() * added + (G + 2) * 2.0 ** -24 * np.abs(c["w"]) + 1e-30
+        assert (np.abs(w - c["w"])[fin] <= lim[fin]).all()
+        assert np.array_equal(np.isnan(w), np.isnan(c["w"]))
+    return o, lse
+
+
+LENS = [0, 1, 15, 16, 17, 31, 63, 64, 65, 127, 128, 129, 200]
+
+
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+@pytest.mark.parametrize("d", [32, 64, 128])
+@pytest.mark.parametrize("H_kv,G", [(1, 1), (3, 2), (2, 7), (2, 8), (1, 9), (1, 16), (2, 17), (1, 40)])
+def test_attention_heads_and_sizes(io, d, H_kv, G):
+    kv, c = cache(LENS, 16, H_kv, d, io, d + G, fill=NAN)
+    q, q64 = query(len(LENS), H_kv * G, d, io, 5)
+    check(kv, c, q, q64, io, d ** -0.5)
+
+
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+@pytest.mark.parametrize("page", [1, 2, 5, 8, 24, 64, 100, 512])
+@pytest.mark.parametrize("layout", ["NHD", "HND", "padded", "interleaved"])
+def test_attention_pages_and_layouts(io, page, layout):
+    lens = [130, 0, 7, 100, 101]
+    kv, c = cache(lens, page, 2, 64, io, page, layout=layout, fill=NAN)
+    q, q64 = query(len(lens), 6, 64, io, 6)
+    check(kv, c, q, q64, io, 0.125, add=True)
+
+
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+@pytest.mark.parametrize("window", [1, 2, 16, 63, 64, 65, 199, 200, 100000])
+@pytest.mark.parametrize("add", [False, True])
+def test_attention_window(io, window, add):
+    """Tokens before the window (NaN here) are not looked at."""
+    kv, c = cache(LENS, 24, 2, 64, io, window)
+    for n, x in enumerate(LENS):
+        for j in range(max(0, x - window)):
+            p, s = paged.place(c, n, j)
+            kv.k[p, s], kv.v[p, s], c["k"][p, s], c["v"][p, s] = NAN, NAN, NAN, NAN
+    q, q64 = query(len(LENS), 8, 64, io, 7)
+    check(kv, c, q, q64, io, 0.125, window, add)
+
+
+@pytest.mark.parametrize("io,N,H_kv,G,d,lens", [
+    ("bf16", 1, 1, 4, 128, (9001,)), ("bf16", 1, 2, 8, 64, (20011,)), ("f32", 1, 1, 3, 128, (7003,)),
+    ("bf16", 3, 2, 1, 32, (12000, 1, 333)), ("f32", 4, 2, 16, 32, (0, 5000, 0, 2)),
+    ("bf16", 2, 1, 33, 128, (4097, 6000)),
+])
+@pytest.mark.parametrize("add", [False, True])
+def test_attention_long_caches_are_split_and_joined(io, N, H_kv, G, d, lens, add):
+    kv, c = cache(list(lens), 16, H_kv, d, io, N + G, fill=NAN)
+    q, q64 = query(N, H_kv * G, d, io, 8)
+    check(kv, c, q, q64, io, d ** -0.5, 0, add)
+
+
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+def test_attention_many_sequences(io):
+    """More sequences than blocks and than one pass of a block's threads over the lengths."""
+    rng = np.random.default_rng(3)
+    lens = [int(x) for x in rng.integers(0, 90, 1500)]
+    kv, c = cache(lens, 8, 1, 32, io, 21, fill=NAN)
+    q, q64 = query(len(lens), 2, 32, io, 9)
+    check(kv, c, q, q64, io, 0.2, 0, True)
+
+
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+def test_attention_large_scores(io):
+    """Scores of several hundred either way: the softmax is nearly one-hot, e^s alone would
+    overflow, and a maximum late in the cache rescales what came before."""
+    kv, c = cache([700, 3, 1], 16, 2, 64, io, 11, fill=NAN)
+    q, q64 = query(3, 8, 64, io, 10, 8.0)
+    check(kv, c, q, q64, io, 2.0, 0, True)
+    check(kv, c, q, q64, io, -2.0)
+    check(kv, c, q, q64, io, 0.0)
+
+
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+def test_attention_infinite_scores(io):
+    """Keys of -inf leave their tokens out, all of them an empty sequence."""
+    kv, c = cache([70, 40], 16, 1, 32, io, 12)
+    q = torch.ones(2, 2, 32).to(DT[io])
+    for n, which in ((0, range(0, 70, 3)), (1, range(40))):
+        for j in which:
+            p, s = paged.place(c, n, j)
+            kv.k[p, s, 0, 0], c["k"][p, s, 0, 0] = float("-inf"), float("-inf")
+    r, rl, a, _ = paged.attention(c, q.double().numpy(), 0.1)
+    o, lse = gdn.attn_decode_step(q.cuda(), kv, scale=0.1, add_weights=True, want_lse=True)
+    assert (o[1] == 0).all() and torch.isneginf(lse[1]).all()
+    got = o.double().cpu().numpy()
+    assert (np.abs(got - r) <= (2.0 ** -7 if io == "bf16" else 1e-5) * (a + np.abs(r)) + 1e-30).all()
+    assert torch.isfinite(kv.weights).all()
+
+
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+def test_attention_nan_stays_in_its_sequence(io):
+    kv, c = cache([50, 50, 50], 16, 2, 32, io, 13)
+    p, s = paged.place(c, 1, 20)
+    kv.k[p, s, 1, 3] = NAN
+    q, _ = query(3, 4, 32, io, 11)
+    o, lse = gdn.attn_decode_step(q, kv, want_lse=True)
+    assert torch.isnan(o[1, 2:]).all() and torch.isnan(lse[1, 2:]).all()
+    assert torch.isfinite(o[0]).all() and torch.isfinite(o[2]).all() and torch.isfinite(o[1, :2]).all()
+
+
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+@pytest.mark.parametrize("add", [False, True])
+def test_attention_bad_pages_and_lengths(io, add):
+    """A page outside the pool is left out, a length outside the table is an empty sequence;
+    both are reported, and the other sequences are right."""
+    lens = [100, 60, 33, 5]
+    kv, c = cache(lens, 16, 2, 64, io, 14, fill=NAN)
+    for t in (c["table"], kv.block_table):
+        t[0, 2], t[0, 6], t[1, 0] = -1, c["k"].shape[0], 2 ** 31 - 1
+    for t in (c["lens"], kv.seq_lens):
+        t[2], t[3] = -4, 16 * c["table"].shape[1] + 1
+    q, q64 = query(4, 4, 64, io, 12)
+    check(kv, c, q, q64, io, 0.125, 0, add, status=1)
+
+
+def test_attention_repeats_bit_for_bit_and_leaves_the_cache():
+    kv, c = cache([3000, 1, 700], 16, 2, 128, "bf16", 15)
+    q, _ = query(3, 16, 128, "bf16", 13)
+    k0, v0 = kv.k.clone(), kv.v.clone()
+    a = gdn.attn_decode_step(q, kv, want_lse=True)
+    b = gdn.attn_decode_step(q, kv, want_lse=True)
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+    assert torch.equal(k0, kv.k) and torch.equal(v0, kv.v)
+
+
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+def test_shared_pages_collect_every_sequences_weight(io):
+    kv, c = cache([48, 48, 20], 16, 2, 32, io, 16)
+    for t in (kv.block_table, c["table"]):
+        t[1, :2] = t[0, :2]
+    q, q64 = query(3, 4, 32, io, 14)
+    check(kv, c, q, q64, io, 0.2, 0, True)
+
+
+# ----------------------------------------------------------------------- append
+
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+@pytest.mark.parametrize("d,H_kv,page,layout", [(32, 1, 1, "NHD"), (64, 3, 24, "HND"), (128, 16, 16, "padded"),
+                                                (128, 2, 7, "interleaved")])
+@pytest.mark.parametrize("in_place", [False, True])
+def test_append_one_token(io, d, H_kv, page, layout, in_place):
+    lens = [0, 1, page - 1, page, 3 * page, 40]
+    kv, c = cache(lens, page, H_kv, d, io, 30 + d, layout=layout, room=1)
+    k, v = (torch.randn(6, H_kv, d, generator=torch.Generator().manual_seed(x)).to(DT[io]) for x in (1, 2))
+    out = None if in_place else torch.full((6,), -3, dtype=torch.int32, device="cuda")
+    gdn.kv_append(kv, k.cuda(), v.cuda(), lens_out=out)
+    assert gdn.gdn2_get_device_status() == 0
+    assert list((kv.seq_lens if in_place else out).cpu()) == [x + 1 for x in lens]
+    if not in_place:
+        assert list(kv.seq_lens.cpu()) == lens
+    paged.append(c, k.double().numpy(), v.double().numpy())
+    h = host(kv)
+    assert all(same(h[x], c[x]) for x in ("k", "v", "w"))   # every other slot as it was
+
+
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+@pytest.mark.parametrize("news", [[3, 0, 41, 1, 0, 100], [0, 0, 0, 0, 0, 0], [1, 1, 1, 1, 1, 1], [0, 0, 0, 0, 0, 1900]])
+@pytest.mark.parametrize("in_place", [False, True])
+def test_append_packed(io, news, in_place):
+    lens = [5, 0, 17, 16, 3, 1]
+    kv, c = cache(lens, 16, 2, 64, io, 31, room=max(news))
+    T = sum(news)
+    k, v = (torch.randn(T, 2, 64, generator=torch.Generator().manual_seed(x)).to(DT[io]) for x in (3, 4))
+    cu = torch.tensor(np.concatenate([[0], np.cumsum(news)]), dtype=torch.int32)
+    out = None if in_place else torch.zeros(6, dtype=torch.int32, device="cuda")
+    gdn.kv_append(kv, k.cuda(), v.cuda(), cu_seqlens=cu.cuda(), lens_out=out)
+    assert gdn.gdn2_get_device_status() == 0
+    assert list((kv.seq_lens if in_place else out).cpu()) == [x + y for x, y in zip(lens, news)]
+    paged.append(c, k.double().numpy(), v.double().numpy(), cu.tolist())
+    h = host(kv)
+    assert all(same(h[x], c[x]) for x in ("k", "v", "w"))
+
+
+def test_append_what_does_not_fit_or_has_no_page():
+    lens = [16, 31, 32, -1, 2 ** 31 - 1]
+    kv, c = cache([16, 31, 32, 0, 0], 16, 2, 32, "f32", 32)
+    kv.block_table[0, 1] = 10 ** 6
+    kv.block_table[1, 1] = -2
+    c["table"][0, 1], c["table"][1, 1] = 10 ** 6, -2
+    kv.seq_lens.copy_(torch.tensor(lens, dtype=torch.int32))
+    c["lens"][:] = lens
+    k = torch.ones(5, 2, 32)
+    paged.append(c, k.double().numpy(), k.double().numpy())
+    gdn.kv_append(kv, k.cuda(), k.cuda())
+    assert gdn.gdn2_get_device_status() == 1
+    h = host(kv)
+    assert all(same(h[x], c[x]) for x in ("k", "v", "w", "lens"))
+    # a table that does not rise appends nothing
+    cu = torch.tensor([0, 3, 2, 4, 4, 5], dtype=torch.int32, device="cuda")
+    gdn.kv_append(kv, k.cuda(), k.cuda(), cu_seqlens=cu)
+    assert gdn.gdn2_get_device_status() == 1
+    h = host(kv)
+    assert all(same(h[x], c[x]) for x in ("k", "v", "w", "lens"))
+
+
+# ------------------------------------------------------------------------ evict
+
+def weighted(kv, c, kind, seed):
+    w = torch.rand(kv.weights.shape, generator=torch.Generator().manual_seed(seed))
+    if kind == "ties":
+        w = torch.floor(w * 4)
+    elif kind == "equal":
+        w = torch.ones_like(w)
+    elif kind == "special":
+        pick = torch.tensor([NAN, float("inf"), float("-inf"), 0.0, -0.0, 1e-40, -1e-40, 3e38, -3e38, 1.0, -1.0])
+        w = pick[(w * len(pick)).long().clamp_max(len(pick) - 1)]
+    elif kind == "close":   # neighbours in float32
+        w = (torch.ones_like(w).view(torch.int32) + (w * 7).int()).view(torch.float32)
+    kv.weights.copy_(w)
+    c["w"][:] = w.double().numpy()
+
+
+@pytest.mark.parametrize("kind", ["random", "ties", "equal", "special", "close"])
+@pytest.mark.parametrize("into", [False, True])
+@pytest.mark.parametrize("budget,sink,recent", [(1, 0, 0), (40, 0, 0), (40, 4, 8), (40, 40, 0), (40, 0, 40), (40, 10, 30),
+                                                (64, 1, 0), (300, 0, 1)])
+def test_evict(kind, into, budget, sink, recent):
+    lens = [0, 1, 39, 40, 41, 64, 65, 300, 301]
+    io, d = ("bf16", 64) if budget != 64 else ("f32", 128)
+    kv, c = cache(lens, 16, 2, d, io, 40, fill=NAN)
+    weighted(kv, c, kind, 1)
+    dst = c2 = None
+    if into:   # another page size and layout
+        dst, c2 = cache([min(x, budget) for x in lens], 5, 2, d, io, 41, layout="HND")
+        dst.seq_lens.fill_(-9)
+        before = host(kv)
+    ref = paged.evict(c, budget, sink, recent, c2)
+    kept = gdn.kv_evict(kv, budget, sink=sink, recent=recent, dst=dst, want_kept=True)
+    assert gdn.gdn2_get_device_status() == 0
+    assert np.array_equal(kept.cpu().numpy(), ref)
+    h = host(dst if into else kv)
+    want = c2 if into else c
+    assert all(same(h[x], want[x]) for x in ("k", "v", "w", "lens"))   # other slots as they were
+    if into:
+        h = host(kv)
+        assert all(same(h[x], before[x]) for x in ("k", "v", "w", "lens"))
+
+
+@pytest.mark.parametrize("io,d,H_kv,page,layout", [("bf16", 32, 1, 1, "NHD"), ("bf16", 128, 3, 24, "padded"),
+                                                   ("f32", 32, 4, 64, "interleaved"), ("f32", 128, 1, 7, "HND")])
+@pytest.mark.parametrize("into", [False, True])
+def test_evict_larger(io, d, H_kv, page, layout, into):
+    lens = [2500, 5, 4096, 3999]
+    kv, c = cache(lens, page, H_kv, d, io, 42, layout=layout)
+    weighted(kv, c, "ties", 2)
+    dst, c2 = cache([min(x, 1999) for x in lens], page, H_kv, d, io, 43, layout=layout) if into else (None, None)
+    ref = paged.evict(c, 1999, 3, 100, c2)
+    kept = gdn.kv_evict(kv, 1999, sink=3, recent=100, dst=dst, want_kept=True)
+    assert np.array_equal(kept.cpu().numpy(), ref)
+    h, want = host(dst if into else kv), c2 if into else c
+    assert all(same(h[x], want[x]) for x in ("k", "v", "w", "lens"))
+    assert gdn.kv_evict(kv, 10 ** 4, dst=None) is None     # within the budget: nothing changes
+    assert list(kv.seq_lens.cpu()) == (lens if into else list(c["lens"]))
+
+
+@pytest.mark.parametrize("length,budget", [(60000, 30000), (120001, 119999)])
+def test_evict_very_long(length, budget):
+    kv, c = cache([length], 64, 1, 32, "bf16", 44)
+    weighted(kv, c, "random", 3)
+    w = np.array([c["w"][paged.place(c, 0, j)[0], 0, paged.place(c, 0, j)[1]] for j in range(length)])
+    k0 = c["k"].copy()
+    kept = gdn.kv_evict(kv, budget, sink=2, recent=64, want_kept=True)[0, 0].cpu().numpy()
+    mid = np.arange(2, length - 64)
+    best = mid[np.lexsort((mid, -w[mid]))[:budget - 66]]
+    assert np.array_equal(kept, np.concatenate([[0, 1], np.sort(best), np.arange(length - 64, length)]))
+    h = host(kv)
+    P = 64
+    new = np.arange(budget)
+    assert np.array_equal(h["k"][c["table"][0, new // P], new % P, 0], k0[c["table"][0, kept // P], kept % P, 0])
+
+
+@pytest.mark.parametrize("into", [False, True])
+def test_evict_bad_pages_and_lengths(into):
+    lens = [100, 60, 33, 5]
+    kv, c = cache(lens, 16, 2, 64, "f32", 45)
+    for t in (c["table"], kv.block_table):
+        t[0, 2], t[1, 0] = -1, 10 ** 7
+    for t in (c["lens"], kv.seq_lens):
+        t[2], t[3] = -4, 16 * c["table"].shape[1] + 1
+    dst, c2 = cache([30, 30, 30, 30], 16, 2, 64, "f32", 46) if into else (None, None)
+    if into:
+        for t in (c2["table"], dst.block_table):
+            t[0, 1] = 10 ** 6
+    ref = paged.evict(c, 30, 2, 5, c2)
+    kept = gdn.kv_evict(kv, 30, sink=2, recent=5, dst=dst, want_kept=True)
+    assert gdn.gdn2_get_device_status() == 1
+    assert np.array_equal(kept.cpu().numpy(), ref)
+    h, want = host(dst if into else kv), c2 if into else c
+    assert all(same(h[x], want[x]) for x in ("k", "v", "w", "lens"))
+
+
+def test_evict_into_a_cache_that_is_too_small():
+    kv, c = cache([50, 20], 16, 1, 32, "f32", 47)
+    dst, c2 = cache([16, 16], 16, 1, 32, "f32", 48)
+    paged.evict(c, 30, 0, 0, c2)
+    gdn.kv_evict(kv, 30, dst=dst)
+    assert gdn.gdn2_get_device_status() == 1
+    h = host(dst)
+    assert all(same(h[x], c2[x]) for x in ("k", "v", "w", "lens"))
+
+
+# ------------------------------------------------- together, streams and graphs
+
+def decode_inputs(N, H, H_kv, d, seed, step):
+    g = torch.Generator().manual_seed(seed * 1000 + step)
+    return tuple(torch.randn(N, h, d, generator=g).to(torch.bfloat16) for h in (H, H_kv, H_kv))
+
+
+@pytest.mark.parametrize("mode", ["plain", "stream", "graph"])
+def test_a_decode_loop_of_both_mixers(mode):
+    """Steps of a hybrid: the recurrent block's step, then the attention block's append and
+    attention with weights, and an eviction whenever 8 tokens are over the budget."""
+    N, H, H_kv, d, budget = 5, 4, 2, 64, 24
+    kv, c = cache([0, 3, 24, 17, 9], 8, H_kv, d, "bf16", 50, room=40, fill=0.0)
+    x = {n: t.cuda() for n, t in workloads.decode_step_inputs(N, H, d, d, 51, 0).items()}
+    S = torch.zeros(N, H, d, d, device="cuda")
+    bufs = [t.cuda() for t in decode_inputs(N, H, H_kv, d, 52, 0)]
+    side = torch.cuda.Stream() if mode == "stream" else None
+    out = {}
+
+    def step():
+        y = gdn.decode_step(x["q"], x["k"], x["v"], x["g"], x["b"], x["w"], S, stream=side)
+        gdn.kv_append(kv, bufs[1], bufs[2], stream=side)
+        out["o"], out["lse"] = gdn.attn_decode_step(bufs[0], kv, add_weights=True, want_lse=True, stream=side)
+        return y
+
+    graph = None
+    if mode == "graph":
+        saved = kv.seq_lens.clone(), kv.weights.clone(), kv.k.clone(), kv.v.clone()
+        step()   # first use of the kernels outside the capture
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            step()
+        for t, s in zip((kv.seq_lens, kv.weights, kv.k, kv.v), saved):
+            t.copy_(s)
+    for i in range(30):
+        q, k, v = decode_inputs(N, H, H_kv, d, 52, i)
+        torch.cuda.synchronize()
+        for b, t in zip(bufs, (q, k, v)):
+            b.copy_(t)
+        torch.cuda.synchronize()
+        graph.replay() if graph else step()
+        torch.cuda.synchronize()
+        paged.append(c, k.double().numpy(), v.double().numpy())
+        r, rl, a, smax = paged.attention(c, q.double().numpy(), d ** -0.5, 0, True)
+        bo, bl, _ = bounds("bf16", r, rl, a, smax, 64, d)
+        assert (np.abs(out["o"].double().cpu().numpy() - r) <= bo).all(), i
+        assert (np.abs(out["lse"].double().cpu().numpy() - rl) <= bl).all(), i
+        h = host(kv)
+        used = np.array([[p for p in (paged.place(c, n, j) for j in range(int(c["lens"][n])))] for n in [2]][0])
+        assert np.allclose(h["w"][used[:, 0], :, used[:, 1]], c["w"][used[:, 0], :, used[:, 1]], rtol=1e-4)
+        if max(c["lens"]) >= budget + 8:
+            c["w"][:] = h["w"]   # the choice is made from the GPU's own sums
+            kept = paged.evict(c, budget, 2, 6)
+            mine = gdn.kv_evict(kv, budget, sink=2, recent=6, want_kept=True, stream=side)
+            torch.cuda.synchronize()
+            assert np.array_equal(mine.cpu().numpy(), kept), i
+        h = host(kv)
+        assert np.array_equal(h["lens"], c["lens"])
+        for n in range(N):
+            for j in range(int(c["lens"][n])):
+                p, s = paged.place(c, n, j)
+                assert np.array_equal(h["k"][p, s], c["k"][p, s]) and np.array_equal(h["v"][p, s], c["v"][p, s])
+    assert gdn.gdn2_get_device_status() == 0
+
+
+def test_two_streams_at_once():
+    """Two caches on two streams, each call with a workspace of its own."""
+    a, ca = cache([4000, 1], 16, 2, 128, "bf16", 60)
+    b, cb = cache([3000, 2000], 16, 2, 128, "bf16", 61)
+    qa, qa64 = query(2, 8, 128, "bf16", 62)
+    qb, qb64 = query(2, 8, 128, "bf16", 63)
+    sa, sb = torch.cuda.Stream(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    res = []
+    for _ in range(20):
+        res.append((gdn.attn_decode_step(qa, a, stream=sa)[0], gdn.attn_decode_step(qb, b, stream=sb)[0]))
+    torch.cuda.synchronize()
+    one = gdn.attn_decode_step(qa, a)[0], gdn.attn_decode_step(qb, b)[0]
+    assert all(torch.equal(x, one[0]) and torch.equal(y, one[1]) for x, y in res)
+    check(a, ca, qa, qa64, "bf16", 128 ** -0.5)
+    check(b, cb, qb, qb64, "bf16", 128 ** -0.5)
+
+
+def test_offsets_beyond_32_bits():
+    """A pool of more than 2^32 bytes (and, float32, 2^30 elements): the last pages are read
+    and written where they are."""
+    if torch.cuda.mem_get_info()[0] < 24 << 30:
+        pytest.skip("needs 24 GB free")
+    pages = (1 << 32) // (16 * 4 * 128 * 2) * 2 + 3    # 8 GB each of k and v
+    k = torch.zeros(pages, 16, 4, 128, dtype=torch.bfloat16, device="cuda")
+    v = torch.zeros_like(k)
+    table = torch.tensor([[pages - 1, 0, pages // 2 + 1, pages - 2]], dtype=torch.int32, device="cuda")
+    w = torch.zeros(pages, 4, 16, device="cuda")
+    kv = gdn.PagedKV(k, v, table, torch.zeros(1, dtype=torch.int32, device="cuda"), w)
+    g = torch.Generator().manual_seed(5)
+    kn, vn = (torch.randn(60, 4, 128, generator=g).to(torch.bfloat16) for _ in range(2))
+    gdn.kv_append(kv, kn.cuda(), vn.cuda(), cu_seqlens=torch.tensor([0, 60], dtype=torch.int32, device="cuda"))
+    small = on_gpu(torch.zeros(4, 16, 4, 128, dtype=torch.bfloat16), torch.zeros(4, 16, 4, 128, dtype=torch.bfloat16),
+                   torch.zeros(4, 4, 16), torch.tensor([[0, 1, 2, 3]], dtype=torch.int32), [0], "NHD")
+    gdn.kv_append(small, kn.cuda(), vn.cuda(), cu_seqlens=torch.tensor([0, 60], dtype=torch.int32, device="cuda"))
+    q, _ = query(1, 8, 128, "bf16", 64)
+    for x in (kv, small):
+        x_o = gdn.attn_decode_step(q, x, add_weights=True)[0]
+        if x is kv:
+            first = x_o
+    assert torch.equal(first, x_o) and float(first.float().abs().max()) > 0
+    assert torch.equal(gdn.kv_evict(kv, 33, sink=1, recent=4, want_kept=True),
+                       gdn.kv_evict(small, 33, sink=1, recent=4, want_kept=True))
+    assert torch.equal(gdn.attn_decode_step(q, kv)[0], gdn.attn_decode_step(q, small)[0])
