@@ -2,96 +2,758 @@
 //
 //   s_j = scale <q, k_j>,  o = sum_j e^(s_j - lse) v_j,  lse = log sum_j e^(s_j)
 //
-// One block per (sequence, key-value head) walks the cached tokens in tiles of
-// 128 with a running maximum m and sum l: a tile's scores raise m, and what
-// was summed before is scaled by e^(m_old - m_new).
+// The call reads each cached k and v once (4 d bytes a token and head in bf16)
+// for 4 d G flops, G query heads sharing them: at most a few flops a byte, so
+// HBM bounds it and everything else has to stay out of the way.
+//
+// Work is cut into units of 64 tokens of one (sequence, key-value head, block
+// of at most 16 query heads), numbered in that order; every block takes an
+// equal run of consecutive units, whatever the sequences' lengths (the lengths
+// are on the device, so each block finds its own run with a scan over them).
+// A block walks the part of its run that lies in one (sequence, head) as a
+// segment with a running maximum m, sum l and accumulator of e^(s - m) v.  A
+// segment that covers the whole (sequence, head) leaves the result, one that
+// does not leaves (m, l, acc) in the workspace; at most the first and the last
+// of a block's segments are such parts.  attn_join combines them:
+//   m = max m_i,  o = sum e^(m_i - m) acc_i / sum e^(m_i - m) l_i.
+// Exponents are in base 2 throughout (scale carries log2 e).
+//
+// Within a block each warp owns 16-token (bf16) or 8-token (float32) slices of
+// its own: it copies their k and v rows into its ring of stages in shared
+// memory with 16-byte asynchronous copies and works on them without a
+// block-wide barrier; the four warps' (m, l, acc) meet once a segment.
 
 #include "paged.cuh"
+#include "tc.cuh"
 
 namespace gdn2 {
 
-constexpr int kAttnThreads = 128;
+constexpr int kAttnWarps = 4;
+constexpr int kAttnThreads = 32 * kAttnWarps;
+constexpr int kUnit = 64;        // tokens of a unit
+constexpr int kHeadBlock = 16;   // query heads of one pass: the M rows of an m16n8k16 product
+constexpr int kStages = 3;
+constexpr int kBlocksPerSm = 2;
+constexpr int kMinUnits = 4;     // fewest units worth a block of their own
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
 
-template <typename E>
-__global__ void __launch_bounds__(kAttnThreads)
-attn_kernel(const PagedView c, const E *q, E *o, float *lse, int H, float scale, int window, int add_weights,
-            unsigned int *status) {
-    __shared__ float sq[kMaxD], sp[kAttnThreads], red[kAttnThreads / 32];
-    __shared__ long long soff[kAttnThreads];
-    const int tid = threadIdx.x, n = blockIdx.x / c.Hkv, kvh = blockIdx.x % c.Hkv, G = H / c.Hkv;
-    const int len = checked_len(c, n, status), first = window > 0 && len > window ? len - window : 0;
-    for (int g = 0; g < G; ++g) {
-        const size_t row = ((size_t)n * H + kvh * G + g) * c.d;
-        __syncthreads();
-        if (tid < c.d) sq[tid] = ldx(q, row + tid);
-        __syncthreads();
-        float m = -INFINITY, l = 0.f, acc = 0.f, L = 0.f;
-        for (int pass = 0; pass <= add_weights; ++pass) {
-            for (int j0 = first; j0 < len; j0 += kAttnThreads) {
-                const int j = j0 + tid;
-                float x = -INFINITY;
-                long long off = -1;
-                size_t wo = 0;
-                if (j < len) {
-                    int entry, slot;
-                    page_slot(c, j, entry, slot);
-                    const int page = page_of(c, n, entry);
-                    if (page < 0) record_status(status, GDN2_ERR_INVALID_ARG);
-                    else {
-                        off = row_off(c, page, slot, kvh);
-                        wo = weight_off(c, page, slot, kvh);
-                        const E *kr = reinterpret_cast<const E *>(c.k + off);
-                        x = 0.f;
-                        for (int i = 0; i < c.d; ++i) x += sq[i] * ldx(kr, i);
-                        x *= scale;
-                    }
-                }
-                if (pass == 1) {
-                    if (off >= 0) atomicAdd(c.w + wo, expf(x - L));
-                    continue;
-                }
-                float mx = x;
-                for (int d = 16; d > 0; d >>= 1) mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, d));
-                if ((tid & 31) == 0) red[tid >> 5] = mx;
-                __syncthreads();
-                mx = fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
-                const float mn = fmaxf(m, mx), base = mn == -INFINITY ? 0.f : mn;
-                sp[tid] = expf(x - base);
-                soff[tid] = off;
-                __syncthreads();
-                const float f = expf(m - base);
-                l *= f;
-                acc *= f;
-                const int cnt = min(kAttnThreads, len - j0);
-                for (int i = 0; i < cnt; ++i) {
-                    l += sp[i];
-                    if (tid < c.d && soff[i] >= 0) acc += sp[i] * ldx(reinterpret_cast<const E *>(c.v + soff[i]), tid);
-                }
-                m = mn;
-                __syncthreads();
-            }
-            if (pass == 0) L = l > 0.f ? m + logf(l) : (l == 0.f ? -INFINITY : l);
-            if (l == 0.f) break;
+struct AttnArgs {
+    PagedView c;
+    const void *q;
+    void *o;
+    float *lse;
+    int H, G, HB, hpb;  // query heads, per kv head, blocks of them, heads of a block
+    float scale2;       // scale log2 e
+    int window;
+    // workspace
+    float2 *ml;         // [2 grid][kHeadBlock] m, l of a part
+    float *part;        // [2 grid][kHeadBlock][d]
+    int2 *parts;        // [N Hkv HB] first and last block with a part, or -1
+    float *lse2;        // [N H] log-sum-exp in base 2 (for the weights), or nullptr
+    float *scores;      // [unit][hpb][kUnit] scores in base 2, or nullptr
+    unsigned int *status;
+};
+
+__device__ __forceinline__ int first_token(int len, int window) { return window > 0 && len > window ? len - window : 0; }
+__device__ __forceinline__ int units_of(const PagedView &c, int n, int window, unsigned int *status) {
+    const int len = checked_len(c, n, status);
+    return (len - first_token(len, window) + kUnit - 1) / kUnit;
+}
+
+// The run of units of block blockIdx.x out of gridDim.x, `per` (= Hkv times
+// head blocks) runs of units a sequence, at least `least` units a block:
+// [u, end) and the sequence n, whose units start at `base`, that u lies in.
+struct Run {
+    long long u, end, share, base;
+    int n;
+};
+template <int NT>
+__device__ __forceinline__ Run find_run(const PagedView &c, int window, int per, int least, unsigned int *status) {
+    __shared__ long long s_warp[NT / 32], s_base;
+    __shared__ int s_n;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    long long x = 0;
+    for (int n = tid; n < c.N; n += NT) x += units_of(c, n, window, status);
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) x += __shfl_xor_sync(0xffffffffu, x, off);
+    if (lane == 0) s_warp[warp] = x;
+    __syncthreads();
+    long long total = 0;
+#pragma unroll
+    for (int i = 0; i < NT / 32; ++i) total += s_warp[i];
+    total *= per;
+    Run r;
+    r.share = (total + gridDim.x - 1) / gridDim.x;
+    if (r.share < least) r.share = least;
+    r.u = r.share * blockIdx.x;
+    r.end = r.u + r.share < total ? r.u + r.share : total;
+    r.base = 0;
+    r.n = 0;
+    if (r.u >= total) return r;  // u >= end: nothing to do
+    long long before = 0;
+    for (int n0 = 0; n0 < c.N; n0 += NT) {
+        const long long mine = n0 + tid < c.N ? units_of(c, n0 + tid, window, status) : 0;
+        long long inc = mine;
+#pragma unroll
+        for (int off = 1; off < 32; off <<= 1) {
+            const long long y = __shfl_up_sync(0xffffffffu, inc, off);
+            if (lane >= off) inc += y;
         }
-        if (tid < c.d) stx(o, row + tid, l == 0.f ? 0.f : acc / l);
-        if (lse && tid == 0) lse[(size_t)n * H + kvh * G + g] = L;
+        __syncthreads();  // s_warp has been read
+        if (lane == 31) s_warp[warp] = inc;
+        __syncthreads();
+        long long all = 0;
+#pragma unroll
+        for (int i = 0; i < NT / 32; ++i) {
+            if (i < warp) inc += s_warp[i];
+            all += s_warp[i];
+        }
+        const long long lo = (before + inc - mine) * per, hi = (before + inc) * per;
+        if (lo <= r.u && r.u < hi) {
+            s_n = n0 + tid;
+            s_base = lo;
+        }
+        before += all;
+        if (before * per > r.u) break;
+    }
+    __syncthreads();
+    r.n = s_n;
+    r.base = s_base;
+    return r;
+}
+
+__device__ __forceinline__ void cp_async16_zfill(uint32_t dst, const void *src, bool valid) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(valid ? 16 : 0) : "memory");
+}
+template <int N> __device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+
+__device__ __forceinline__ void ldmatrix4(uint32_t addr, uint32_t *r) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+__device__ __forceinline__ void ldmatrix4_trans(uint32_t addr, uint32_t *r) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+// d += a b: a 16 x 16 (row), b 16 x 8 (column), bf16, float32 sums
+__device__ __forceinline__ void mma16816(float *d, const uint32_t *a, uint32_t b0, uint32_t b1) {
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                 : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// A segment: tokens [begin, end) of sequence n, key-value head h, and query
+// heads [head, head + rows).
+struct Segment {
+    int n, h, head, rows, begin, end;
+    long long unit;  // the number of its first unit
+};
+
+// A warp's ring of stages and its copies.  Step i of the segment covers tokens
+// begin + (i kAttnWarps + warp) KW + 0 .. KW-1.  A stage holds KW rows of k,
+// then KW of v, rows of RB bytes with their 16-byte pieces permuted by the row
+// (piece p of row r at p ^ key(r)), so that eight rows' equal pieces lie in
+// different banks.  Rows without a token are zeros: their v must not be
+// whatever the memory held, since 0 times NaN is NaN.
+template <int KW, int RB>
+struct Ring {
+    static constexpr int kPieces = RB / 16;
+    static constexpr int kHalf = KW * RB, kStage = 2 * kHalf;
+    static constexpr int kBytes = kStages * kStage;
+    const PagedView &c;
+    const Segment &sg;
+    uint32_t base;  // this warp's stages
+    int warp, lane, steps;
+    uint32_t live[kStages];  // which of a stage's rows hold a token
+    unsigned int *status;
+
+    __device__ __forceinline__ static int key(int r) { return kPieces >= 8 ? r & 7 : (r >> 1) & (kPieces - 1); }
+    __device__ __forceinline__ static uint32_t at(int r, int piece) { return (uint32_t)(r * RB + ((piece ^ key(r)) << 4)); }
+
+    // the pool offset of row `lane % KW` of step i, -1 where it holds no token
+    __device__ __forceinline__ long long lookup(int i) const {
+        const int j = sg.begin + (i * kAttnWarps + warp) * KW + lane % KW;
+        if (i >= steps || j >= sg.end) return -1;
+        int entry, slot;
+        page_slot(c, j, entry, slot);
+        const int page = page_of(c, sg.n, entry);
+        if (page < 0) {
+            record_status(status, GDN2_ERR_INVALID_ARG);
+            return -1;
+        }
+        return row_off(c, page, slot, sg.h);
+    }
+    // starts step i's copies (a group of its own, empty past the last step)
+    __device__ __forceinline__ void issue(int i, int stage, long long off) {
+        const uint32_t ok = __ballot_sync(0xffffffffu, off >= 0);
+        live[stage] = ok;
+        if (i < steps) {
+            const uint32_t s = base + stage * kStage;
+            constexpr int kRowsAtOnce = 32 / kPieces > KW ? KW : 32 / kPieces;  // rows of one instruction
+            static_assert(KW * kPieces % 32 == 0, "whole warps of pieces");
+#pragma unroll
+            for (int x = 0; x < KW * kPieces / 32; ++x) {
+                const int r = x * kRowsAtOnce + lane / kPieces, piece = lane % kPieces;
+                const long long ro = __shfl_sync(0xffffffffu, off, r);
+                const long long from = (ro < 0 ? 0 : ro) + piece * 16;
+                cp_async16_zfill(s + at(r, piece), c.k + from, ro >= 0);
+                cp_async16_zfill(s + kHalf + at(r, piece), c.v + from, ro >= 0);
+            }
+        }
+        tc::cp_async_commit();
+    }
+};
+
+// ---- bf16: products on the tensor cores, the query heads as the 16 rows.  Of
+// the instruction's rows only the group's are used; at a few flops a byte the
+// rest costs nothing that is missed.
+template <int D>
+struct EngineBf16 {
+    using E = __nv_bfloat16;
+    static constexpr int KW = 16, RB = 2 * D, kRows = 16;
+    uint32_t qf[D / 16][4];
+    float acc[D / 8][4];
+    float m[2], l[2];
+
+    __device__ __forceinline__ void begin(const AttnArgs &a, const Segment &sg, int lane, float *) {
+        const E *q = static_cast<const E *>(a.q) + ((size_t)sg.n * a.H + sg.head) * D;
+        const int g = lane >> 2, t = lane & 3;
+#pragma unroll
+        for (int s = 0; s < D / 16; ++s)
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+                const int row = g + (x & 1) * 8, col = s * 16 + (x >> 1) * 8 + 2 * t;
+                qf[s][x] = row < sg.rows ? *reinterpret_cast<const uint32_t *>(q + row * D + col) : 0u;
+            }
+#pragma unroll
+        for (int i = 0; i < D / 8; ++i) acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.f;
+        m[0] = m[1] = -INFINITY;
+        l[0] = l[1] = 0.f;
+    }
+    // one step of 16 tokens; `scores`: this step's place for rows of kUnit scores, or nullptr
+    __device__ __forceinline__ void step(const AttnArgs &a, const Segment &sg, uint32_t ks, uint32_t vs, uint32_t live,
+                                         int lane, float *scores, float *) {
+        using R = Ring<KW, RB>;
+        float s[2][4] = {};
+        const int mi = lane >> 3, lr = lane & 7, t = lane & 3;
+#pragma unroll
+        for (int x = 0; x < D / 16; ++x) {
+            uint32_t b[4];  // tokens 0..7: k pieces 2x, 2x+1; tokens 8..15: the same
+            ldmatrix4(ks + R::at((mi >> 1) * 8 + lr, 2 * x + (mi & 1)), b);
+            mma16816(s[0], qf[x], b[0], b[1]);
+            mma16816(s[1], qf[x], b[2], b[3]);
+        }
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int x = 0; x < 4; ++x) s[i][x] *= a.scale2;
+        if ((live & 0xffffu) != 0xffffu) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+#pragma unroll
+                for (int x = 0; x < 4; ++x)
+                    if (!(live >> (i * 8 + 2 * t + (x & 1)) & 1u)) s[i][x] = -INFINITY;
+        }
+        if (scores) {
+            const int g = lane >> 2;
+#pragma unroll
+            for (int y = 0; y < 2; ++y)
+                if (g + y * 8 < sg.rows)
+#pragma unroll
+                    for (int i = 0; i < 2; ++i)
+                        *reinterpret_cast<float2 *>(scores + (g + y * 8) * kUnit + i * 8 + 2 * t) =
+                            make_float2(s[i][2 * y], s[i][2 * y + 1]);
+        }
+        float mx[2], mn[2];
+#pragma unroll
+        for (int y = 0; y < 2; ++y) {
+            mx[y] = fmaxf(fmaxf(s[0][2 * y], s[0][2 * y + 1]), fmaxf(s[1][2 * y], s[1][2 * y + 1]));
+            mx[y] = fmaxf(mx[y], __shfl_xor_sync(0xffffffffu, mx[y], 1));
+            mx[y] = fmaxf(mx[y], __shfl_xor_sync(0xffffffffu, mx[y], 2));
+            mn[y] = fmaxf(m[y], mx[y]);
+        }
+        if (__any_sync(0xffffffffu, mn[0] > m[0] || mn[1] > m[1])) {
+#pragma unroll
+            for (int y = 0; y < 2; ++y) {
+                const float f = mn[y] == m[y] ? 1.f : exp2f(m[y] - mn[y]);  // -inf - -inf is not a number
+                m[y] = mn[y];
+                l[y] *= f;
+#pragma unroll
+                for (int i = 0; i < D / 8; ++i) {
+                    acc[i][2 * y] *= f;
+                    acc[i][2 * y + 1] *= f;
+                }
+            }
+        }
+        uint32_t p[4];
+#pragma unroll
+        for (int y = 0; y < 2; ++y) {
+            const float ref = m[y] == -INFINITY ? 0.f : m[y];
+            float e[2][2];
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    e[i][x] = exp2f(s[i][2 * y + x] - ref);
+                    l[y] += e[i][x];
+                }
+            // the only rounding on the way: weights in [0, 1] to bf16, the type of
+            // the v that they multiply; the sum takes them unrounded
+            p[y] = tc::pack_bf16(e[0][0], e[0][1]);
+            p[2 + y] = tc::pack_bf16(e[1][0], e[1][1]);
+        }
+#pragma unroll
+        for (int x = 0; x < D / 16; ++x) {
+            uint32_t b[4];  // channels 16x..+7 and +8..+15, tokens 0..7 and 8..15
+            ldmatrix4_trans(vs + R::at((mi & 1) * 8 + lr, 2 * x + (mi >> 1)), b);
+            mma16816(acc[2 * x], p, b[0], b[1]);
+            mma16816(acc[2 * x + 1], p, b[2], b[3]);
+        }
+    }
+    // this warp's m, l [kRows] and acc [kRows][D + 8] to shared memory
+    __device__ __forceinline__ void finish(float2 *ml, float *out, int lane) {
+        const int g = lane >> 2, t = lane & 3;
+#pragma unroll
+        for (int y = 0; y < 2; ++y) {
+            l[y] += __shfl_xor_sync(0xffffffffu, l[y], 1);
+            l[y] += __shfl_xor_sync(0xffffffffu, l[y], 2);
+            if (t == 0) ml[g + 8 * y] = make_float2(m[y], l[y]);
+#pragma unroll
+            for (int i = 0; i < D / 8; ++i)
+                *reinterpret_cast<float2 *>(out + (g + 8 * y) * (D + 8) + i * 8 + 2 * t) =
+                    make_float2(acc[i][2 * y], acc[i][2 * y + 1]);
+        }
+    }
+};
+
+// ---- float32: products on the CUDA cores (the tensor cores' tf32 would lose
+// what a float32 cache is kept for).  Scores: lane (part, token) = (lane / 8,
+// lane % 8) sums a quarter of the channels; values: a lane owns four channels
+// of every (128 / D)-th token.  GP: query heads, padded to a power of two.
+template <int D, int GP>
+struct EngineF32 {
+    using E = float;
+    static constexpr int KW = 8, RB = 4 * D, kRows = GP;
+    static constexpr int kLanes = D / 4;        // lanes of one token's channels
+    static constexpr int kGroups = 32 / kLanes;  // tokens at once
+    float acc[GP][4];
+    float m[GP], l[GP];
+
+    // sq: [GP][D] of the block's
+    __device__ __forceinline__ void begin(const AttnArgs &a, const Segment &sg, int, float *sq) {
+        const float *q = static_cast<const float *>(a.q) + ((size_t)sg.n * a.H + sg.head) * D;
+        __syncthreads();
+        for (int i = threadIdx.x; i < GP * D; i += kAttnThreads) sq[i] = i < sg.rows * D ? q[i] : 0.f;
+        __syncthreads();
+#pragma unroll
+        for (int g = 0; g < GP; ++g) {
+            acc[g][0] = acc[g][1] = acc[g][2] = acc[g][3] = 0.f;
+            m[g] = -INFINITY;
+            l[g] = 0.f;
+        }
+    }
+    // sp: [kWarps][GP][KW] behind sq
+    __device__ __forceinline__ void step(const AttnArgs &a, const Segment &sg, uint32_t ks, uint32_t vs, uint32_t live,
+                                         int lane, float *scores, float *sq) {
+        using R = Ring<KW, RB>;
+        float *sp = sq + GP * D + (threadIdx.x >> 5) * GP * KW;
+        const int tok = lane & 7, part = lane >> 3;
+        float s[GP];
+#pragma unroll
+        for (int g = 0; g < GP; ++g) s[g] = 0.f;
+#pragma unroll
+        for (int x = 0; x < D / 16; ++x) {
+            const int piece = 4 * x + part;
+            const float4 k = ld4(ks + R::at(tok, piece));
+#pragma unroll
+            for (int g = 0; g < GP; ++g) {
+                const float4 q = *reinterpret_cast<const float4 *>(sq + g * D + piece * 4);
+                s[g] = fmaf(k.x, q.x, fmaf(k.y, q.y, fmaf(k.z, q.z, fmaf(k.w, q.w, s[g]))));
+            }
+        }
+        bool raised = false;
+        float mn[GP];
+        const bool on = live >> tok & 1u;
+#pragma unroll
+        for (int g = 0; g < GP; ++g) {
+            s[g] += __shfl_xor_sync(0xffffffffu, s[g], 8);
+            s[g] += __shfl_xor_sync(0xffffffffu, s[g], 16);
+            s[g] = on ? s[g] * a.scale2 : -INFINITY;
+            mn[g] = s[g];
+#pragma unroll
+            for (int off = 1; off < 8; off <<= 1) mn[g] = fmaxf(mn[g], __shfl_xor_sync(0xffffffffu, mn[g], off));
+            mn[g] = fmaxf(m[g], mn[g]);
+            raised |= mn[g] > m[g];
+        }
+        if (scores && part == 0)
+#pragma unroll
+            for (int g = 0; g < GP; ++g)
+                if (g < sg.rows) scores[g * kUnit + tok] = s[g];
+        if (raised) {  // the same on every lane: m and mn are
+#pragma unroll
+            for (int g = 0; g < GP; ++g) {
+                const float f = mn[g] == m[g] ? 1.f : exp2f(m[g] - mn[g]);
+                m[g] = mn[g];
+                l[g] *= f;
+                acc[g][0] *= f; acc[g][1] *= f; acc[g][2] *= f; acc[g][3] *= f;
+            }
+        }
+        __syncwarp();  // the last step's sp has been read
+#pragma unroll
+        for (int g = 0; g < GP; ++g) {
+            if (GP >= 4 && (g & 3) != part) continue;  // shared out among the four parts
+            const float e = exp2f(s[g] - (m[g] == -INFINITY ? 0.f : m[g]));
+            l[g] += e;
+            if (GP >= 4 || part == 0) sp[g * KW + tok] = e;
+        }
+        __syncwarp();
+        const int grp = lane / kLanes, ch = lane % kLanes;
+#pragma unroll
+        for (int x = 0; x < KW / kGroups; ++x) {
+            const int r = x * kGroups + grp;
+            const float4 v = ld4(vs + R::at(r, ch));
+#pragma unroll
+            for (int g = 0; g < GP; ++g) {
+                const float e = sp[g * KW + r];
+                acc[g][0] = fmaf(e, v.x, acc[g][0]);
+                acc[g][1] = fmaf(e, v.y, acc[g][1]);
+                acc[g][2] = fmaf(e, v.z, acc[g][2]);
+                acc[g][3] = fmaf(e, v.w, acc[g][3]);
+            }
+        }
+    }
+    __device__ __forceinline__ void finish(float2 *ml, float *out, int lane) {
+        const int part = lane >> 3, ch = lane % kLanes;
+#pragma unroll
+        for (int g = 0; g < GP; ++g) {
+            // a row's sum lies with one part's lanes (or, the same, with all four)
+            float x = GP >= 4 ? ((g & 3) == part ? l[g] : 0.f) : (part == 0 ? l[g] : 0.f);
+#pragma unroll
+            for (int off = 1; off < 32; off <<= 1) x += __shfl_xor_sync(0xffffffffu, x, off);
+            if (lane == 0) ml[g] = make_float2(m[g], x);
+#pragma unroll
+            for (int off = kLanes; off < 32; off <<= 1)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) acc[g][i] += __shfl_xor_sync(0xffffffffu, acc[g][i], off);
+            if (lane < kLanes)
+                *reinterpret_cast<float4 *>(out + g * (D + 8) + ch * 4) =
+                    make_float4(acc[g][0], acc[g][1], acc[g][2], acc[g][3]);
+        }
+    }
+    __device__ __forceinline__ static float4 ld4(uint32_t addr) {
+        float4 v;
+        asm volatile("ld.shared.v4.f32 {%0,%1,%2,%3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr) : "memory");
+        return v;
+    }
+};
+
+__device__ __forceinline__ void store4(float *p, float4 v) { *reinterpret_cast<float4 *>(p) = v; }
+__device__ __forceinline__ void store4(__nv_bfloat16 *p, float4 v) {
+    *reinterpret_cast<uint2 *>(p) = make_uint2(tc::pack_bf16(v.x, v.y), tc::pack_bf16(v.z, v.w));
+}
+
+// shared memory of a block: the warps' rings, or (between segments) their
+// (m, l, acc); then what the engine keeps
+template <class En, int D> constexpr int attn_smem() {
+    constexpr int ring = kAttnWarps * Ring<En::KW, En::RB>::kBytes;
+    constexpr int merge = kAttnWarps * En::kRows * (8 + 4 * (D + 8));
+    constexpr int own = sizeof(typename En::E) == 4 ? En::kRows * (D + kAttnWarps * En::KW) * 4 : 0;
+    return (ring > merge ? ring : merge) + own;
+}
+
+template <class En, int D>
+__global__ void __launch_bounds__(kAttnThreads, kBlocksPerSm)
+attn_split_kernel(const AttnArgs a) {
+    extern __shared__ __align__(128) unsigned char smem[];
+    using R = Ring<En::KW, En::RB>;
+    using E = typename En::E;
+    constexpr int kRing = kAttnWarps * R::kBytes, kMerge = kAttnWarps * En::kRows * (8 + 4 * (D + 8));
+    float *own = reinterpret_cast<float *>(smem + (kRing > kMerge ? kRing : kMerge));
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const PagedView &c = a.c;
+    const int per = c.Hkv * a.HB;
+    Run run = find_run<kAttnThreads>(c, a.window, per, kMinUnits, a.status);
+    En en;
+    while (run.u < run.end) {
+        const int len = checked_len(c, run.n, a.status), first = first_token(len, a.window);
+        const int T = (len - first + kUnit - 1) / kUnit;
+        if (T == 0) {
+            ++run.n;
+            continue;
+        }
+        const int r = (int)((run.u - run.base) / T), t0 = (int)((run.u - run.base) - (long long)r * T);
+        const int cnt = (int)(T - t0 < run.end - run.u ? T - t0 : run.end - run.u);
+        Segment sg;
+        sg.n = run.n;
+        sg.h = r / a.HB;
+        const int hb = r - sg.h * a.HB;
+        sg.head = sg.h * a.G + hb * a.hpb;
+        sg.rows = min(a.hpb, a.G - hb * a.hpb);
+        sg.begin = first + t0 * kUnit;
+        sg.end = min(len, sg.begin + cnt * kUnit);
+        sg.unit = run.u;
+
+        constexpr int kStep = kAttnWarps * En::KW;
+        R ring{c, sg, tc::smem_addr(smem) + warp * R::kBytes, warp, lane, (sg.end - sg.begin + kStep - 1) / kStep, {}, a.status};
+        long long next = ring.lookup(0);
+#pragma unroll
+        for (int s = 0; s < kStages - 1; ++s) {
+            const long long off = next;
+            next = ring.lookup(s + 1);
+            ring.issue(s, s, off);
+        }
+        en.begin(a, sg, lane, own);
+        for (int i0 = 0; i0 < ring.steps; i0 += kStages) {
+#pragma unroll
+            for (int s = 0; s < kStages; ++s) {
+                const int i = i0 + s;
+                if (i >= ring.steps) break;
+                __syncwarp();  // the stage that the next copies go to has been read
+                const long long off = next;
+                next = ring.lookup(i + kStages);
+                ring.issue(i + kStages - 1, (s + kStages - 1) % kStages, off);
+                cp_async_wait<kStages - 1>();
+                __syncwarp();
+                const int tok = (i * kAttnWarps + warp) * En::KW;  // in the segment
+                float *sc = a.scores ? a.scores + ((sg.unit + tok / kUnit) * a.hpb) * kUnit + tok % kUnit : nullptr;
+                const uint32_t st = ring.base + s * R::kStage;
+                if (ring.live[s]) en.step(a, sg, st, st + R::kHalf, ring.live[s], lane, sc, own);
+            }
+        }
+        cp_async_wait<0>();
+        __syncthreads();  // every warp is done with its ring
+        float2 *ml = reinterpret_cast<float2 *>(smem);
+        float *po = reinterpret_cast<float *>(smem + kAttnWarps * En::kRows * 8);
+        en.finish(ml + warp * En::kRows, po + warp * En::kRows * (D + 8), lane);
+        __syncthreads();
+        const bool whole = t0 == 0 && cnt == T;
+        const int slot = 2 * blockIdx.x + (t0 == 0);
+        for (int x = tid; x < sg.rows * (D / 4); x += kAttnThreads) {
+            const int row = x / (D / 4), ch = (x - row * (D / 4)) * 4;
+            float m = -INFINITY, l = 0.f;
+#pragma unroll
+            for (int w = 0; w < kAttnWarps; ++w) m = fmaxf(m, ml[w * En::kRows + row].x);
+            float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+            for (int w = 0; w < kAttnWarps; ++w) {
+                const float2 y = ml[w * En::kRows + row];
+                const float f = y.x == -INFINITY ? (y.y == 0.f ? 0.f : 1.f) : exp2f(y.x - m);
+                const float4 v = *reinterpret_cast<const float4 *>(po + (w * En::kRows + row) * (D + 8) + ch);
+                l += f * y.y;
+                o.x += f * v.x; o.y += f * v.y; o.z += f * v.z; o.w += f * v.w;
+            }
+            if (whole) {
+                const float inv = l == 0.f ? 0.f : 1.f / l;
+                const size_t hd = (size_t)sg.n * a.H + sg.head + row;
+                store4(static_cast<E *>(a.o) + hd * D + ch, l == 0.f ? make_float4(0.f, 0.f, 0.f, 0.f)
+                                                                  : make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv));
+                if (ch == 0) {
+                    const float L = l == 0.f ? -INFINITY : m + log2f(l);
+                    if (a.lse) a.lse[hd] = l == 0.f ? -INFINITY : m * kLn2 + logf(l);
+                    if (a.lse2) a.lse2[hd] = L;
+                }
+            } else {
+                store4(a.part + ((size_t)slot * kHeadBlock + row) * D + ch, o);
+                if (ch == 0) a.ml[(size_t)slot * kHeadBlock + row] = make_float2(m, l);
+            }
+        }
+        if (tid == 0 && t0 == 0)
+            a.parts[(size_t)sg.n * per + r] =
+                whole ? make_int2(-1, -1)
+                      : make_int2((int)blockIdx.x, (int)((run.base + (long long)(r + 1) * T - 1) / run.share));
+        __syncthreads();  // the merge area is the rings' again
+        run.u += cnt;
+        if (run.u == run.base + (long long)per * T) {
+            run.base = run.u;
+            ++run.n;
+        }
     }
 }
 
-size_t attn_ws_bytes(const PagedView &, int, int) { return 256; }
+// One block a (sequence, query head): joins its parts, or writes the empty
+// sequence's result, or (no parts: it is written already) ends.
+template <typename E, int D>
+__global__ void __launch_bounds__(kAttnThreads)
+attn_join_kernel(const AttnArgs a) {
+    constexpr int kLanes = D / 4, kGroups = kAttnThreads / kLanes;
+    __shared__ float s_m[kAttnThreads / 32];
+    __shared__ float s_l[kGroups];
+    __shared__ float4 s_o[kGroups][kLanes];
+    const int tid = threadIdx.x, n = blockIdx.x / a.H, h = blockIdx.x - n * a.H, kvh = h / a.G, g = h - kvh * a.G;
+    const int hb = g / a.hpb, row = g - hb * a.hpb;
+    const size_t hd = blockIdx.x;
+    E *o = static_cast<E *>(a.o) + hd * D;
+    if (checked_len(a.c, n, a.status) == 0) {
+        if (tid < kLanes) store4(o + tid * 4, make_float4(0.f, 0.f, 0.f, 0.f));
+        if (tid == 0) {
+            if (a.lse) a.lse[hd] = -INFINITY;
+            if (a.lse2) a.lse2[hd] = -INFINITY;
+        }
+        return;
+    }
+    const int2 pr = a.parts[((size_t)n * a.c.Hkv + kvh) * a.HB + hb];
+    if (pr.x < 0) return;
+    // block pr.x has the run's beginning (its second part), the others their first
+    auto slot = [&](int b) { return (size_t)(2 * b + (b == pr.x)) * kHeadBlock + row; };
+    float m = -INFINITY;
+    for (int b = pr.x + tid; b <= pr.y; b += kAttnThreads) m = fmaxf(m, a.ml[slot(b)].x);
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
+    if ((tid & 31) == 0) s_m[tid >> 5] = m;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < kAttnThreads / 32; ++w) m = fmaxf(m, s_m[w]);
+    const int grp = tid / kLanes, ch = tid - grp * kLanes;
+    float l = 0.f;
+    float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int b = pr.x + grp; b <= pr.y; b += kGroups) {
+        const float2 y = a.ml[slot(b)];
+        const float4 v = *reinterpret_cast<const float4 *>(a.part + slot(b) * D + ch * 4);
+        const float f = y.x == -INFINITY ? (y.y == 0.f ? 0.f : 1.f) : exp2f(y.x - m);
+        l += f * y.y;
+        x.x += f * v.x; x.y += f * v.y; x.z += f * v.z; x.w += f * v.w;
+    }
+    if (ch == 0) s_l[grp] = l;
+    s_o[grp][ch] = x;
+    __syncthreads();
+    if (tid >= kLanes) return;
+    l = 0.f;
+    x = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int i = 0; i < kGroups; ++i) {
+        const float4 v = s_o[i][tid];
+        l += s_l[i];
+        x.x += v.x; x.y += v.y; x.z += v.z; x.w += v.w;
+    }
+    const float inv = 1.f / l;
+    store4(o + tid * 4, l == 0.f ? make_float4(0.f, 0.f, 0.f, 0.f) : make_float4(x.x * inv, x.y * inv, x.z * inv, x.w * inv));
+    if (tid == 0) {
+        if (a.lse) a.lse[hd] = l == 0.f ? -INFINITY : m * kLn2 + logf(l);
+        if (a.lse2) a.lse2[hd] = l == 0.f ? -INFINITY : m + log2f(l);
+    }
+}
+
+// weight_j += sum over the group's heads of 2^(s_j - lse), from the scores the
+// split kernel kept: 64 threads a unit, a token each.  One addition a token and
+// call, so the sums do not depend on any order unless sequences share a page.
+__global__ void __launch_bounds__(kAttnThreads)
+attn_weights_kernel(const AttnArgs a) {
+    const PagedView &c = a.c;
+    Run run = find_run<kAttnThreads>(c, a.window, c.Hkv, 2, a.status);
+    const int half = threadIdx.x / kUnit, tok = threadIdx.x % kUnit;
+    while (run.u < run.end) {
+        const int len = checked_len(c, run.n, a.status), first = first_token(len, a.window);
+        const int T = (len - first + kUnit - 1) / kUnit;
+        if (T == 0) {
+            ++run.n;
+            continue;
+        }
+        const int h = (int)((run.u - run.base) / T), t0 = (int)((run.u - run.base) - (long long)h * T);
+        const int cnt = (int)(T - t0 < run.end - run.u ? T - t0 : run.end - run.u);
+        const float *L = a.lse2 + (size_t)run.n * a.H + h * a.G;
+        for (int t = t0 + half; t < t0 + cnt; t += kAttnThreads / kUnit) {
+            const int j = first + t * kUnit + tok;
+            if (j >= len) continue;
+            int entry, slot;
+            page_slot(c, j, entry, slot);
+            const int page = page_of(c, run.n, entry);
+            if (page < 0) continue;
+            float sum = 0.f;
+            for (int hb = 0; hb < a.HB; ++hb) {
+                // the split kernel's number of this unit: `per` = Hkv HB runs a sequence
+                const long long unit = run.base * a.HB + ((long long)h * a.HB + hb) * T + t;
+                const float *s = a.scores + unit * a.hpb * kUnit + tok;
+                const int rows = min(a.hpb, a.G - hb * a.hpb);
+                for (int r = 0; r < rows; ++r) {
+                    const float Lr = L[hb * a.hpb + r];
+                    sum += Lr == -INFINITY ? 0.f : exp2f(s[r * kUnit] - Lr);
+                }
+            }
+            atomicAdd(c.w + weight_off(c, page, slot, h), sum);
+        }
+        run.u += cnt;
+        if (run.u == run.base + (long long)c.Hkv * T) {
+            run.base = run.u;
+            ++run.n;
+        }
+    }
+}
+
+// ---- host side
+static void head_blocks(const PagedView &c, int H, AttnArgs &a) {
+    a.H = H;
+    a.G = H / c.Hkv;
+    a.HB = (a.G + kHeadBlock - 1) / kHeadBlock;
+    a.hpb = (a.G + a.HB - 1) / a.HB;
+}
+
+// places the workspace's regions (ws may be null: sizes only); returns its bytes
+static size_t attn_ws(const PagedView &c, AttnArgs &a, int add_weights, void *ws) {
+    const size_t slots = 2 * (size_t)kBlocksPerSm * sm_count(), runs = (size_t)c.N * c.Hkv * a.HB;
+    size_t o = 0;
+    auto take = [&](size_t bytes) { const size_t at = o; o = align256(o + bytes); return static_cast<char *>(ws) + at; };
+    a.ml = reinterpret_cast<float2 *>(take(slots * kHeadBlock * sizeof(float2)));
+    a.part = reinterpret_cast<float *>(take(slots * kHeadBlock * c.d * sizeof(float)));
+    a.parts = reinterpret_cast<int2 *>(take(runs * sizeof(int2)));
+    a.lse2 = a.scores = nullptr;
+    if (add_weights) {
+        a.lse2 = reinterpret_cast<float *>(take((size_t)c.N * a.H * sizeof(float)));
+        a.scores = reinterpret_cast<float *>(take(runs * ((c.cap + kUnit - 1) / kUnit) * a.hpb * kUnit * sizeof(float)));
+    }
+    return o;
+}
+
+size_t attn_ws_bytes(const PagedView &c, int H, int add_weights) {
+    AttnArgs a;
+    head_blocks(c, H, a);
+    return attn_ws(c, a, add_weights, nullptr);
+}
+
+template <class En, int D>
+static cudaError_t attn_run(const AttnArgs &a, cudaStream_t s) {
+    constexpr int bytes = attn_smem<En, D>();
+    cudaError_t e = cudaFuncSetAttribute(attn_split_kernel<En, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e != cudaSuccess) return e;
+    launch_begin(K_ATTN_SPLIT, s);
+    attn_split_kernel<En, D><<<kBlocksPerSm * sm_count(), kAttnThreads, bytes, s>>>(a);
+    launch_end(K_ATTN_SPLIT, s);
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    launch_begin(K_ATTN_JOIN, s);
+    attn_join_kernel<typename En::E, D><<<a.c.N * a.H, kAttnThreads, 0, s>>>(a);
+    launch_end(K_ATTN_JOIN, s);
+    if ((e = cudaGetLastError()) != cudaSuccess || !a.scores) return e;
+    launch_begin(K_ATTN_WEIGHTS, s);
+    attn_weights_kernel<<<4 * sm_count(), kAttnThreads, 0, s>>>(a);
+    launch_end(K_ATTN_WEIGHTS, s);
+    return cudaGetLastError();
+}
+
+template <int D>
+static cudaError_t attn_for_d(const AttnArgs &a, cudaStream_t s) {
+    if (a.c.es == 2) return attn_run<EngineBf16<D>, D>(a, s);
+    if (a.hpb == 1) return attn_run<EngineF32<D, 1>, D>(a, s);
+    if (a.hpb == 2) return attn_run<EngineF32<D, 2>, D>(a, s);
+    if (a.hpb <= 4) return attn_run<EngineF32<D, 4>, D>(a, s);
+    if (a.hpb <= 8) return attn_run<EngineF32<D, 8>, D>(a, s);
+    return attn_run<EngineF32<D, 16>, D>(a, s);
+}
 
 cudaError_t attn_launch(const PagedView &c, const void *q, void *o, float *lse, int H, float scale, int window,
-                        int add_weights, void *, unsigned int *status, cudaStream_t s) {
-    launch_begin(K_ATTN_SPLIT, s);
-    if (c.es == 2)
-        attn_kernel<<<c.N * c.Hkv, kAttnThreads, 0, s>>>(c, static_cast<const __nv_bfloat16 *>(q),
-                                                         static_cast<__nv_bfloat16 *>(o), lse, H, scale, window,
-                                                         add_weights, status);
-    else
-        attn_kernel<<<c.N * c.Hkv, kAttnThreads, 0, s>>>(c, static_cast<const float *>(q), static_cast<float *>(o),
-                                                         lse, H, scale, window, add_weights, status);
-    launch_end(K_ATTN_SPLIT, s);
-    return cudaGetLastError();
+                        int add_weights, void *ws, unsigned int *status, cudaStream_t s) {
+    AttnArgs a;
+    a.c = c;
+    a.q = q;
+    a.o = o;
+    a.lse = lse;
+    head_blocks(c, H, a);
+    a.scale2 = scale * kLog2e;
+    a.window = window;
+    a.status = status;
+    attn_ws(c, a, add_weights, ws);
+    if (c.d == 32) return attn_for_d<32>(a, s);
+    if (c.d == 64) return attn_for_d<64>(a, s);
+    return attn_for_d<128>(a, s);
 }
 
 }  // namespace gdn2
