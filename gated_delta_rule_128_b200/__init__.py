@@ -156,6 +156,11 @@ def _gate_io_of(g: torch.Tensor, b: torch.Tensor, w: torch.Tensor, gates: str = 
     raise TypeError(f"g/b/w must be float32 or bfloat16, got {g.dtype}")
 
 
+def _raw_stream(device: int) -> int:
+    """The current stream of a device, as cudaStream_t."""
+    return torch._C._cuda_getCurrentRawStream(device)
+
+
 def _stream(stream=None):
     s = torch.cuda.current_stream() if stream is None else stream
     return ctypes.c_void_p(s.cuda_stream)
@@ -441,14 +446,23 @@ def decode_step(q, k, v, g, b, w, S, o=None, stream=None, gates: str = "activate
 # ------------------------------------------------------- paged key-value cache
 
 def _tensor(name: str, t: torch.Tensor, dtype, shape, device) -> None:
+    if t.dtype is dtype and t.shape == shape and t.device == device and t.is_contiguous():
+        return
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if tuple(t.shape) != tuple(shape):
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
     if t.device != device:
         raise ValueError(f"{name} is on {t.device}, the cache on {device}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
+    raise ValueError(f"{name} must be contiguous")
+
+
+def _workspace(ws: Optional[torch.Tensor], n: int, device) -> torch.Tensor:
+    if ws is None:
+        return torch.empty(n, dtype=torch.uint8, device=device)
+    if ws.device != device or not ws.is_contiguous():
+        raise ValueError(f"ws must be contiguous, on {device}")
+    return ws
 
 
 class PagedKV:
@@ -496,6 +510,7 @@ class PagedKV:
         self._ws_bytes = {}  # workspace sizes, by what they depend on
 
     def workspace_bytes(self, fn: str, *args) -> int:
+        """The size that a call's workspace query returns for this cache."""
         n = self._ws_bytes.get((fn, args))
         if n is None:
             n = globals()[fn](self, *args)
@@ -505,6 +520,9 @@ class PagedKV:
         return n
 
 
+_HERE = contextlib.nullcontext()
+
+
 def _on_stream(kv: PagedKV, stream):
     """A context in which the cache's device is current, and `stream` too where
     one is given, so that what is allocated inside belongs to that stream."""
@@ -512,12 +530,11 @@ def _on_stream(kv: PagedKV, stream):
         if stream.device != kv.device:
             raise ValueError(f"the stream is on {stream.device}, the cache on {kv.device}")
         return torch.cuda.stream(stream)
+    if kv.device.type != "cuda":
+        raise ValueError(f"the cache is on {kv.device}: its calls need a CUDA device")
     if torch.cuda.current_device() != kv.device.index:
         return torch.cuda.device(kv.device)
     return _HERE
-
-
-_HERE = contextlib.nullcontext()
 
 
 def kv_append(kv: PagedKV, k, v, *, cu_seqlens=None, lens_out=None, stream=None) -> None:
@@ -527,8 +544,9 @@ def kv_append(kv: PagedKV, k, v, *, cu_seqlens=None, lens_out=None, stream=None)
     find wrong in the tables is read with check_device_status."""
     s = kv.struct
     T = k.shape[0]
-    _tensor("k", k, kv.k.dtype, (T, s.H_kv, s.d), kv.device)
-    _tensor("v", v, kv.k.dtype, (T, s.H_kv, s.d), kv.device)
+    shape = (T, s.H_kv, s.d)
+    _tensor("k", k, kv.k.dtype, shape, kv.device)
+    _tensor("v", v, kv.k.dtype, shape, kv.device)
     if cu_seqlens is not None:
         _tensor("cu_seqlens", cu_seqlens, torch.int32, (s.N + 1,), kv.device)
     if lens_out is None:
@@ -536,7 +554,11 @@ def kv_append(kv: PagedKV, k, v, *, cu_seqlens=None, lens_out=None, stream=None)
     else:
         _tensor("lens_out", lens_out, torch.int32, (s.N,), kv.device)
     with _on_stream(kv, stream):
-        gdn2_kv_append(kv, k, v, cu_seqlens, T, lens_out)
+        rc = lib().gdn2_kv_append(kv.ref, k.data_ptr(), v.data_ptr(),
+                                  None if cu_seqlens is None else cu_seqlens.data_ptr(), T,
+                                  lens_out.data_ptr(), _raw_stream(kv.device.index))
+    if rc:
+        raise Gdn2Error("gdn2_kv_append", rc)
 
 
 def attn_decode_step(q, kv: PagedKV, *, scale: Optional[float] = None, window: int = 0,
@@ -546,23 +568,26 @@ def attn_decode_step(q, kv: PagedKV, *, scale: Optional[float] = None, window: i
     head h reading key-value head h // (H // H_kv).  scale: 1/sqrt(d) unless
     given.  add_weights=True adds each token's softmax weights to kv.weights.
     Returns (o [N,H,d], lse float32 [N,H] or None).  Asynchronous, as
-    decode_step."""
+    decode_step.  ws: scratch of kv.workspace_bytes(
+    "gdn2_attn_decode_workspace_bytes", H, add_weights) bytes, allocated unless
+    given; calls that may run at once need one each."""
     s = kv.struct
     if q.dim() != 3:
         raise ValueError(f"q must have shape [N, H, d], got {tuple(q.shape)}")
     H = q.shape[1]
     _tensor("q", q, kv.k.dtype, (s.N, H, s.d), kv.device)
+    if o is not None:
+        _tensor("o", o, q.dtype, q.shape, kv.device)
     with _on_stream(kv, stream):
         if o is None:
             o = torch.empty_like(q)
-        else:
-            _tensor("o", o, q.dtype, q.shape, kv.device)
         lse = torch.empty((s.N, H), dtype=torch.float32, device=kv.device) if want_lse else None
-        if ws is None:
-            ws = torch.empty(kv.workspace_bytes("gdn2_attn_decode_workspace_bytes", H, bool(add_weights)),
-                             dtype=torch.uint8, device=kv.device)
-        gdn2_attn_decode_step(kv, q, o, lse, H, s.d ** -0.5 if scale is None else scale, window,
-                              add_weights, ws, ws.numel())
+        ws = _workspace(ws, kv.workspace_bytes("gdn2_attn_decode_workspace_bytes", H, bool(add_weights)), kv.device)
+        rc = lib().gdn2_attn_decode_step(kv.ref, q.data_ptr(), o.data_ptr(), None if lse is None else lse.data_ptr(),
+                                         H, s.d ** -0.5 if scale is None else scale, window, bool(add_weights),
+                                         ws.data_ptr(), ws.nbytes, _raw_stream(kv.device.index))
+    if rc:
+        raise Gdn2Error("gdn2_attn_decode_step", rc)
     return o, lse
 
 
@@ -576,11 +601,14 @@ def kv_evict(kv: PagedKV, budget: int, *, sink: int = 0, recent: int = 0, dst: O
     s = kv.struct
     if dst is not None and dst.device != kv.device:
         raise ValueError(f"dst is on {dst.device}, the cache on {kv.device}")
+    if budget < 1:
+        raise ValueError(f"budget must be at least 1, got {budget}")
     with _on_stream(kv, stream):
-        kept = (torch.empty((s.N, s.H_kv, budget), dtype=torch.int32, device=kv.device)
-                if want_kept and budget > 0 else None)
-        if ws is None:
-            ws = torch.empty(kv.workspace_bytes("gdn2_kv_evict_workspace_bytes", budget) if budget > 0 else 256,
-                             dtype=torch.uint8, device=kv.device)
-        gdn2_kv_evict(kv, dst, budget, sink, recent, kept, ws, ws.numel())
+        kept = torch.empty((s.N, s.H_kv, budget), dtype=torch.int32, device=kv.device) if want_kept else None
+        ws = _workspace(ws, kv.workspace_bytes("gdn2_kv_evict_workspace_bytes", budget), kv.device)
+        rc = lib().gdn2_kv_evict(kv.ref, None if dst is None else dst.ref, budget, sink, recent,
+                                 None if kept is None else kept.data_ptr(), ws.data_ptr(), ws.nbytes,
+                                 _raw_stream(kv.device.index))
+    if rc:
+        raise Gdn2Error("gdn2_kv_evict", rc)
     return kept

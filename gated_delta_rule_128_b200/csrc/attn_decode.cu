@@ -34,7 +34,10 @@ constexpr int kUnit = 64;        // tokens of a unit
 constexpr int kHeadBlock = 16;   // query heads of one pass: the M rows of an m16n8k16 product
 constexpr int kStages = 3;
 constexpr int kBlocksPerSm = 2;
-constexpr int kMinUnits = 4;     // fewest units worth a block of their own
+constexpr int kMinUnits = 2;     // fewest units worth a block of their own
+// Tables that reach no further than this give each block one (sequence, head)
+// whole: no search for a run, no join.
+constexpr int kSoloTokens = 256;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
@@ -73,15 +76,23 @@ __device__ __forceinline__ Run find_run(const PagedView &c, int window, int per,
     __shared__ long long s_warp[NT / 32], s_base;
     __shared__ int s_n;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    long long x = 0;
-    for (int n = tid; n < c.N; n += NT) x += units_of(c, n, window, status);
+    long long x = 0, mine = 0;
+    for (int n = tid; n < c.N; n += NT) x += mine = units_of(c, n, window, status);
+    long long inc = x;
 #pragma unroll
-    for (int off = 16; off > 0; off >>= 1) x += __shfl_xor_sync(0xffffffffu, x, off);
-    if (lane == 0) s_warp[warp] = x;
+    for (int off = 1; off < 32; off <<= 1) {
+        const long long y = __shfl_up_sync(0xffffffffu, inc, off);
+        if (lane >= off) inc += y;
+    }
+    if (lane == 31) s_warp[warp] = inc;
     __syncthreads();
     long long total = 0;
 #pragma unroll
-    for (int i = 0; i < NT / 32; ++i) total += s_warp[i];
+    for (int i = 0; i < NT / 32; ++i) {
+        if (i < warp) inc += s_warp[i];
+        total += s_warp[i];
+    }
+    const long long all_units = total;
     total *= per;
     Run r;
     r.share = (total + gridDim.x - 1) / gridDim.x;
@@ -91,23 +102,24 @@ __device__ __forceinline__ Run find_run(const PagedView &c, int window, int per,
     r.base = 0;
     r.n = 0;
     if (r.u >= total) return r;  // u >= end: nothing to do
-    long long before = 0;
-    for (int n0 = 0; n0 < c.N; n0 += NT) {
-        const long long mine = n0 + tid < c.N ? units_of(c, n0 + tid, window, status) : 0;
-        long long inc = mine;
+    long long before = 0, all = all_units;
+    for (int n0 = 0;;) {  // chunks of NT sequences; the only one's scan is the one above
+        if (c.N > NT) {
+            inc = mine = n0 + tid < c.N ? units_of(c, n0 + tid, window, status) : 0;
 #pragma unroll
-        for (int off = 1; off < 32; off <<= 1) {
-            const long long y = __shfl_up_sync(0xffffffffu, inc, off);
-            if (lane >= off) inc += y;
-        }
-        __syncthreads();  // s_warp has been read
-        if (lane == 31) s_warp[warp] = inc;
-        __syncthreads();
-        long long all = 0;
+            for (int off = 1; off < 32; off <<= 1) {
+                const long long y = __shfl_up_sync(0xffffffffu, inc, off);
+                if (lane >= off) inc += y;
+            }
+            __syncthreads();  // s_warp has been read
+            if (lane == 31) s_warp[warp] = inc;
+            __syncthreads();
+            all = 0;
 #pragma unroll
-        for (int i = 0; i < NT / 32; ++i) {
-            if (i < warp) inc += s_warp[i];
-            all += s_warp[i];
+            for (int i = 0; i < NT / 32; ++i) {
+                if (i < warp) inc += s_warp[i];
+                all += s_warp[i];
+            }
         }
         const long long lo = (before + inc - mine) * per, hi = (before + inc) * per;
         if (lo <= r.u && r.u < hi) {
@@ -115,7 +127,8 @@ __device__ __forceinline__ Run find_run(const PagedView &c, int window, int per,
             s_base = lo;
         }
         before += all;
-        if (before * per > r.u) break;
+        n0 += NT;
+        if (before * per > r.u || n0 >= c.N) break;
     }
     __syncthreads();
     r.n = s_n;
@@ -453,6 +466,22 @@ __device__ __forceinline__ void store4(__nv_bfloat16 *p, float4 v) {
     *reinterpret_cast<uint2 *>(p) = make_uint2(tc::pack_bf16(v.x, v.y), tc::pack_bf16(v.z, v.w));
 }
 
+// what a part with maximum and sum (m, l) = y counts for at the joint maximum m
+// (a part of nothing has none; one of not-a-numbers keeps them)
+__device__ __forceinline__ float part_factor(float2 y, float m) {
+    return y.x == -INFINITY ? (y.y == 0.f ? 0.f : 1.f) : exp2f(y.x - m);
+}
+// four channels of o, and (first: once a head) the log-sum-exp
+template <typename E>
+__device__ __forceinline__ void write_result(const AttnArgs &a, E *o, size_t hd, bool first, float m, float l, float4 x) {
+    const bool none = l == 0.f;
+    const float inv = none ? 0.f : 1.f / l;
+    store4(o, none ? make_float4(0.f, 0.f, 0.f, 0.f) : make_float4(x.x * inv, x.y * inv, x.z * inv, x.w * inv));
+    if (!first) return;
+    if (a.lse) a.lse[hd] = none ? -INFINITY : m * kLn2 + logf(l);
+    if (a.lse2) a.lse2[hd] = none ? -INFINITY : m + log2f(l);
+}
+
 // shared memory of a block: the warps' rings, or (between segments) their
 // (m, l, acc); then what the engine keeps
 template <class En, int D> constexpr int attn_smem() {
@@ -462,7 +491,8 @@ template <class En, int D> constexpr int attn_smem() {
     return (ring > merge ? ring : merge) + own;
 }
 
-template <class En, int D>
+// SOLO: block b takes run b whole (no parts, no join).
+template <class En, int D, bool SOLO>
 __global__ void __launch_bounds__(kAttnThreads, kBlocksPerSm)
 attn_split_kernel(const AttnArgs a) {
     extern __shared__ __align__(128) unsigned char smem[];
@@ -473,17 +503,28 @@ attn_split_kernel(const AttnArgs a) {
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const PagedView &c = a.c;
     const int per = c.Hkv * a.HB;
-    Run run = find_run<kAttnThreads>(c, a.window, per, kMinUnits, a.status);
+    allow_next_launch();
+    Run run;
+    if constexpr (SOLO) {
+        run.n = blockIdx.x / per;
+        run.u = 0;
+        run.end = 1;
+    } else run = find_run<kAttnThreads>(c, a.window, per, kMinUnits, a.status);
     En en;
     while (run.u < run.end) {
         const int len = checked_len(c, run.n, a.status), first = first_token(len, a.window);
         const int T = (len - first + kUnit - 1) / kUnit;
-        if (T == 0) {
-            ++run.n;
-            continue;
+        int r, t0 = 0, cnt = T;
+        if constexpr (SOLO) r = blockIdx.x - run.n * per;
+        else {
+            if (T == 0) {
+                ++run.n;
+                continue;
+            }
+            r = (int)((run.u - run.base) / T);
+            t0 = (int)((run.u - run.base) - (long long)r * T);
+            cnt = (int)(T - t0 < run.end - run.u ? T - t0 : run.end - run.u);
         }
-        const int r = (int)((run.u - run.base) / T), t0 = (int)((run.u - run.base) - (long long)r * T);
-        const int cnt = (int)(T - t0 < run.end - run.u ? T - t0 : run.end - run.u);
         Segment sg;
         sg.n = run.n;
         sg.h = r / a.HB;
@@ -492,7 +533,7 @@ attn_split_kernel(const AttnArgs a) {
         sg.rows = min(a.hpb, a.G - hb * a.hpb);
         sg.begin = first + t0 * kUnit;
         sg.end = min(len, sg.begin + cnt * kUnit);
-        sg.unit = run.u;
+        sg.unit = SOLO ? (long long)blockIdx.x * ((c.cap + kUnit - 1) / kUnit) : run.u;
 
         constexpr int kStep = kAttnWarps * En::KW;
         R ring{c, sg, tc::smem_addr(smem) + warp * R::kBytes, warp, lane, (sg.end - sg.begin + kStep - 1) / kStep, {}, a.status};
@@ -527,7 +568,7 @@ attn_split_kernel(const AttnArgs a) {
         float *po = reinterpret_cast<float *>(smem + kAttnWarps * En::kRows * 8);
         en.finish(ml + warp * En::kRows, po + warp * En::kRows * (D + 8), lane);
         __syncthreads();
-        const bool whole = t0 == 0 && cnt == T;
+        const bool whole = SOLO || (t0 == 0 && cnt == T);
         const int slot = 2 * blockIdx.x + (t0 == 0);
         for (int x = tid; x < sg.rows * (D / 4); x += kAttnThreads) {
             const int row = x / (D / 4), ch = (x - row * (D / 4)) * 4;
@@ -538,26 +579,20 @@ attn_split_kernel(const AttnArgs a) {
 #pragma unroll
             for (int w = 0; w < kAttnWarps; ++w) {
                 const float2 y = ml[w * En::kRows + row];
-                const float f = y.x == -INFINITY ? (y.y == 0.f ? 0.f : 1.f) : exp2f(y.x - m);
+                const float f = part_factor(y, m);
                 const float4 v = *reinterpret_cast<const float4 *>(po + (w * En::kRows + row) * (D + 8) + ch);
                 l += f * y.y;
                 o.x += f * v.x; o.y += f * v.y; o.z += f * v.z; o.w += f * v.w;
             }
             if (whole) {
-                const float inv = l == 0.f ? 0.f : 1.f / l;
                 const size_t hd = (size_t)sg.n * a.H + sg.head + row;
-                store4(static_cast<E *>(a.o) + hd * D + ch, l == 0.f ? make_float4(0.f, 0.f, 0.f, 0.f)
-                                                                  : make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv));
-                if (ch == 0) {
-                    const float L = l == 0.f ? -INFINITY : m + log2f(l);
-                    if (a.lse) a.lse[hd] = l == 0.f ? -INFINITY : m * kLn2 + logf(l);
-                    if (a.lse2) a.lse2[hd] = L;
-                }
+                write_result(a, static_cast<E *>(a.o) + hd * D + ch, hd, ch == 0, m, l, o);
             } else {
                 store4(a.part + ((size_t)slot * kHeadBlock + row) * D + ch, o);
                 if (ch == 0) a.ml[(size_t)slot * kHeadBlock + row] = make_float2(m, l);
             }
         }
+        if constexpr (SOLO) return;
         if (tid == 0 && t0 == 0)
             a.parts[(size_t)sg.n * per + r] =
                 whole ? make_int2(-1, -1)
@@ -572,18 +607,23 @@ attn_split_kernel(const AttnArgs a) {
 }
 
 // One block a (sequence, query head): joins its parts, or writes the empty
-// sequence's result, or (no parts: it is written already) ends.
+// sequence's result, or (no parts: it is written already) ends.  Each of the
+// block's groups of D / 4 lanes takes every kGroups-th part, four loads ahead
+// (one sequence alone leaves a part in every block).
+constexpr int kJoinThreads = 256;
 template <typename E, int D>
-__global__ void __launch_bounds__(kAttnThreads)
+__global__ void __launch_bounds__(kJoinThreads)
 attn_join_kernel(const AttnArgs a) {
-    constexpr int kLanes = D / 4, kGroups = kAttnThreads / kLanes;
-    __shared__ float s_m[kAttnThreads / 32];
+    constexpr int kLanes = D / 4, kGroups = kJoinThreads / kLanes, kAhead = 4;
+    __shared__ float s_m[kJoinThreads / 32];
     __shared__ float s_l[kGroups];
     __shared__ float4 s_o[kGroups][kLanes];
     const int tid = threadIdx.x, n = blockIdx.x / a.H, h = blockIdx.x - n * a.H, kvh = h / a.G, g = h - kvh * a.G;
     const int hb = g / a.hpb, row = g - hb * a.hpb;
     const size_t hd = blockIdx.x;
     E *o = static_cast<E *>(a.o) + hd * D;
+    allow_next_launch();
+    wait_for_previous();
     if (checked_len(a.c, n, a.status) == 0) {
         if (tid < kLanes) store4(o + tid * 4, make_float4(0.f, 0.f, 0.f, 0.f));
         if (tid == 0) {
@@ -596,23 +636,38 @@ attn_join_kernel(const AttnArgs a) {
     if (pr.x < 0) return;
     // block pr.x has the run's beginning (its second part), the others their first
     auto slot = [&](int b) { return (size_t)(2 * b + (b == pr.x)) * kHeadBlock + row; };
+    const int grp = tid / kLanes, ch = tid - grp * kLanes;
+    float4 v[kAhead];
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {  // the first parts come while the maximum is found
+        const int b = pr.x + grp + i * kGroups;
+        if (b <= pr.y) v[i] = *reinterpret_cast<const float4 *>(a.part + slot(b) * D + ch * 4);
+    }
     float m = -INFINITY;
-    for (int b = pr.x + tid; b <= pr.y; b += kAttnThreads) m = fmaxf(m, a.ml[slot(b)].x);
+    for (int b = pr.x + tid; b <= pr.y; b += kJoinThreads) m = fmaxf(m, a.ml[slot(b)].x);
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
     if ((tid & 31) == 0) s_m[tid >> 5] = m;
     __syncthreads();
 #pragma unroll
-    for (int w = 0; w < kAttnThreads / 32; ++w) m = fmaxf(m, s_m[w]);
-    const int grp = tid / kLanes, ch = tid - grp * kLanes;
+    for (int w = 0; w < kJoinThreads / 32; ++w) m = fmaxf(m, s_m[w]);
     float l = 0.f;
     float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int b = pr.x + grp; b <= pr.y; b += kGroups) {
-        const float2 y = a.ml[slot(b)];
-        const float4 v = *reinterpret_cast<const float4 *>(a.part + slot(b) * D + ch * 4);
-        const float f = y.x == -INFINITY ? (y.y == 0.f ? 0.f : 1.f) : exp2f(y.x - m);
-        l += f * y.y;
-        x.x += f * v.x; x.y += f * v.y; x.z += f * v.z; x.w += f * v.w;
+    for (int b0 = pr.x + grp; b0 <= pr.y; b0 += kAhead * kGroups) {
+        float2 y[kAhead];
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) {
+            const int b = b0 + i * kGroups;
+            y[i] = b <= pr.y ? a.ml[slot(b)] : make_float2(-INFINITY, 0.f);
+            if (b0 != pr.x + grp && b <= pr.y) v[i] = *reinterpret_cast<const float4 *>(a.part + slot(b) * D + ch * 4);
+        }
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) {
+            if (b0 + i * kGroups > pr.y) break;
+            const float f = part_factor(y[i], m);
+            l += f * y[i].y;
+            x.x += f * v[i].x; x.y += f * v[i].y; x.z += f * v[i].z; x.w += f * v[i].w;
+        }
     }
     if (ch == 0) s_l[grp] = l;
     s_o[grp][ch] = x;
@@ -622,25 +677,22 @@ attn_join_kernel(const AttnArgs a) {
     x = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
     for (int i = 0; i < kGroups; ++i) {
-        const float4 v = s_o[i][tid];
+        const float4 w = s_o[i][tid];
         l += s_l[i];
-        x.x += v.x; x.y += v.y; x.z += v.z; x.w += v.w;
+        x.x += w.x; x.y += w.y; x.z += w.z; x.w += w.w;
     }
-    const float inv = 1.f / l;
-    store4(o + tid * 4, l == 0.f ? make_float4(0.f, 0.f, 0.f, 0.f) : make_float4(x.x * inv, x.y * inv, x.z * inv, x.w * inv));
-    if (tid == 0) {
-        if (a.lse) a.lse[hd] = l == 0.f ? -INFINITY : m * kLn2 + logf(l);
-        if (a.lse2) a.lse2[hd] = l == 0.f ? -INFINITY : m + log2f(l);
-    }
+    write_result(a, o + tid * 4, hd, tid == 0, m, l, x);
 }
 
 // weight_j += sum over the group's heads of 2^(s_j - lse), from the scores the
 // split kernel kept: 64 threads a unit, a token each.  One addition a token and
 // call, so the sums do not depend on any order unless sequences share a page.
-__global__ void __launch_bounds__(kAttnThreads)
-attn_weights_kernel(const AttnArgs a) {
+constexpr int kWeightThreads = 256;
+__global__ void __launch_bounds__(kWeightThreads)
+attn_weights_kernel(const AttnArgs a, int solo) {
     const PagedView &c = a.c;
-    Run run = find_run<kAttnThreads>(c, a.window, c.Hkv, 2, a.status);
+    wait_for_previous();
+    Run run = find_run<kWeightThreads>(c, a.window, c.Hkv, 1, a.status);
     const int half = threadIdx.x / kUnit, tok = threadIdx.x % kUnit;
     while (run.u < run.end) {
         const int len = checked_len(c, run.n, a.status), first = first_token(len, a.window);
@@ -652,7 +704,7 @@ attn_weights_kernel(const AttnArgs a) {
         const int h = (int)((run.u - run.base) / T), t0 = (int)((run.u - run.base) - (long long)h * T);
         const int cnt = (int)(T - t0 < run.end - run.u ? T - t0 : run.end - run.u);
         const float *L = a.lse2 + (size_t)run.n * a.H + h * a.G;
-        for (int t = t0 + half; t < t0 + cnt; t += kAttnThreads / kUnit) {
+        for (int t = t0 + half; t < t0 + cnt; t += kWeightThreads / kUnit) {
             const int j = first + t * kUnit + tok;
             if (j >= len) continue;
             int entry, slot;
@@ -661,8 +713,10 @@ attn_weights_kernel(const AttnArgs a) {
             if (page < 0) continue;
             float sum = 0.f;
             for (int hb = 0; hb < a.HB; ++hb) {
-                // the split kernel's number of this unit: `per` = Hkv HB runs a sequence
-                const long long unit = run.base * a.HB + ((long long)h * a.HB + hb) * T + t;
+                // the split kernel's number of this unit: it has Hkv HB runs a sequence
+                const long long run_of = (long long)h * a.HB + hb;
+                const long long unit = solo ? ((long long)run.n * c.Hkv * a.HB + run_of) * ((c.cap + kUnit - 1) / kUnit) + t
+                                            : run.base * a.HB + run_of * T + t;
                 const float *s = a.scores + unit * a.hpb * kUnit + tok;
                 const int rows = min(a.hpb, a.G - hb * a.hpb);
                 for (int r = 0; r < rows; ++r) {
@@ -710,23 +764,23 @@ size_t attn_ws_bytes(const PagedView &c, int H, int add_weights) {
     return attn_ws(c, a, add_weights, nullptr);
 }
 
-template <class En, int D>
-static cudaError_t attn_run(const AttnArgs &a, cudaStream_t s) {
+template <class En, int D, bool SOLO>
+static cudaError_t attn_run_as(const AttnArgs &a, cudaStream_t s) {
     constexpr int bytes = attn_smem<En, D>();
-    cudaError_t e = cudaFuncSetAttribute(attn_split_kernel<En, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    cudaError_t e = cudaFuncSetAttribute(attn_split_kernel<En, D, SOLO>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
     if (e != cudaSuccess) return e;
     launch_begin(K_ATTN_SPLIT, s);
-    attn_split_kernel<En, D><<<kBlocksPerSm * sm_count(), kAttnThreads, bytes, s>>>(a);
+    attn_split_kernel<En, D, SOLO><<<SOLO ? a.c.N * a.c.Hkv * a.HB : kBlocksPerSm * sm_count(), kAttnThreads, bytes, s>>>(a);
     launch_end(K_ATTN_SPLIT, s);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
-    launch_begin(K_ATTN_JOIN, s);
-    attn_join_kernel<typename En::E, D><<<a.c.N * a.H, kAttnThreads, 0, s>>>(a);
-    launch_end(K_ATTN_JOIN, s);
-    if ((e = cudaGetLastError()) != cudaSuccess || !a.scores) return e;
-    launch_begin(K_ATTN_WEIGHTS, s);
-    attn_weights_kernel<<<4 * sm_count(), kAttnThreads, 0, s>>>(a);
-    launch_end(K_ATTN_WEIGHTS, s);
-    return cudaGetLastError();
+    if (!SOLO && (e = launch_behind(K_ATTN_JOIN, attn_join_kernel<typename En::E, D>, a.c.N * a.H, kJoinThreads, 0, s, a)) != cudaSuccess)
+        return e;
+    if (!a.scores) return cudaSuccess;
+    return launch_behind(K_ATTN_WEIGHTS, attn_weights_kernel, 8 * sm_count(), kWeightThreads, 0, s, a, (int)SOLO);
+}
+template <class En, int D>
+static cudaError_t attn_run(const AttnArgs &a, cudaStream_t s) {
+    return a.c.cap <= kSoloTokens ? attn_run_as<En, D, true>(a, s) : attn_run_as<En, D, false>(a, s);
 }
 
 template <int D>

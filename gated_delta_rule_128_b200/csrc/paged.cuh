@@ -46,6 +46,32 @@ __device__ __forceinline__ int checked_len(const PagedView &c, int n, unsigned i
     return 0;
 }
 
+// The kernels of one call follow each other on the stream without waiting for
+// the launch: a kernel allows the next one's blocks to come up at once, and
+// those wait, before their first access, until it has finished.
+__device__ __forceinline__ void allow_next_launch() { asm volatile("griddepcontrol.launch_dependents;"); }
+__device__ __forceinline__ void wait_for_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
+// launches a kernel whose blocks come up while the one before it still runs
+// (they wait for it themselves)
+template <typename... P, typename... A>
+static cudaError_t launch_behind(int kind, void (*kernel)(P...), int grid, int threads, int smem, cudaStream_t s, A... args) {
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    launch_begin(kind, s);
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, P(args)...);
+    launch_end(kind, s);
+    return e;
+}
+
 cudaError_t kv_append_launch(const PagedView &c, const void *k, const void *v, const int *cu, int T,
                              int *lens_out, unsigned int *status, cudaStream_t s);
 size_t attn_ws_bytes(const PagedView &c, int H, int add_weights);

@@ -165,6 +165,10 @@ def test_binding_refuses_arguments(L):
         gdn.kv_append(kv, torch.zeros(3, 2, 32), torch.zeros(3, 1, 32))
     with pytest.raises(TypeError):
         gdn.kv_append(kv, torch.zeros(3, 2, 32), torch.zeros(3, 2, 32), cu_seqlens=torch.zeros(4, dtype=torch.int64))
+    with pytest.raises(ValueError, match="CUDA"):
+        gdn.attn_decode_step(torch.zeros(3, 4, 32), kv)
+    with pytest.raises(ValueError, match="budget"):
+        gdn.kv_evict(kv, 0)
     with pytest.raises(ValueError):
         gdn.kv_append(kv, torch.zeros(3, 2, 32), torch.zeros(3, 2, 32), lens_out=torch.zeros(2, dtype=torch.int32))
 
