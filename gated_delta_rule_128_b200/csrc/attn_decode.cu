@@ -21,7 +21,8 @@
 // Within a block each warp owns 16-token (bf16) or 8-token (float32) slices of
 // its own: it copies their k and v rows into its ring of stages in shared
 // memory with 16-byte asynchronous copies and works on them without a
-// block-wide barrier; the four warps' (m, l, acc) meet once a segment.
+// block-wide barrier; the four warps' (m, l, acc) meet once a segment.  The
+// copies run ahead across segments, so a merge does not empty the ring.
 
 #include "paged.cuh"
 #include "tc.cuh"
@@ -31,9 +32,9 @@ namespace gdn2 {
 constexpr int kAttnWarps = 4;
 constexpr int kAttnThreads = 32 * kAttnWarps;
 constexpr int kUnit = 64;        // tokens of a unit
-constexpr int kHeadBlock = 16;   // query heads of one pass: the M rows of an m16n8k16 product
+constexpr int kMostBlocksPerSm = 4;
+constexpr int kHeadBlock = 16;   // most query heads of one pass
 constexpr int kStages = 3;
-constexpr int kBlocksPerSm = 2;
 constexpr int kMinUnits = 2;     // fewest units worth a block of their own
 // Tables that reach no further than this give each block one (sequence, head)
 // whole: no search for a run, no join.
@@ -149,6 +150,12 @@ __device__ __forceinline__ void ldmatrix4_trans(uint32_t addr, uint32_t *r) {
     asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
                  : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
 }
+// an 8 x 8 block of 16-bit values (thread 4 r + c holds row r, columns 2c, 2c + 1), transposed
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
+    uint32_t y;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    return y;
+}
 // d += a b: a 16 x 16 (row), b 16 x 8 (column), bf16, float32 sums
 __device__ __forceinline__ void mma16816(float *d, const uint32_t *a, uint32_t b0, uint32_t b1) {
     asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
@@ -160,183 +167,268 @@ __device__ __forceinline__ void mma16816(float *d, const uint32_t *a, uint32_t b
 // heads [head, head + rows).
 struct Segment {
     int n, h, head, rows, begin, end;
-    long long unit;  // the number of its first unit
+    int run;             // (h, head block) in the sequence
+    bool starts, whole;  // it starts at the run's first unit, and covers it
+    long long unit;      // the number of its first unit
+    long long run_end;   // one past the run's last unit
 };
+// the next segment of a run of units (false: there is none)
+template <bool SOLO>
+__device__ __forceinline__ bool next_segment(const AttnArgs &a, Run &run, Segment &sg) {
+    const PagedView &c = a.c;
+    const int per = c.Hkv * a.HB;
+    while (run.u < run.end) {
+        const int len = checked_len(c, run.n, a.status), first = first_token(len, a.window);
+        const int T = (len - first + kUnit - 1) / kUnit;
+        int t0 = 0, cnt = T;
+        if constexpr (SOLO) {
+            sg.run = blockIdx.x - run.n * per;
+            sg.unit = (long long)blockIdx.x * ((c.cap + kUnit - 1) / kUnit);
+            run.u = run.end;
+        } else {
+            if (T == 0) {
+                ++run.n;
+                continue;
+            }
+            const long long in = run.u - run.base, left = run.end - run.u;
+            sg.run = (int)(in < 0x7fffffffLL ? (unsigned)in / (unsigned)T : in / T);
+            t0 = (int)(in - (long long)sg.run * T);
+            cnt = (int)(T - t0 < left ? T - t0 : left);
+            sg.unit = run.u;
+            sg.run_end = run.base + (long long)(sg.run + 1) * T;
+        }
+        sg.n = run.n;
+        sg.h = sg.run / a.HB;
+        const int hb = sg.run - sg.h * a.HB;
+        sg.head = sg.h * a.G + hb * a.hpb;
+        sg.rows = min(a.hpb, a.G - hb * a.hpb);
+        sg.begin = first + t0 * kUnit;
+        sg.end = min(len, sg.begin + cnt * kUnit);
+        sg.starts = t0 == 0;
+        sg.whole = t0 == 0 && cnt == T;
+        if constexpr (!SOLO) {
+            run.u += cnt;
+            if (run.u == run.base + (long long)per * T) {
+                run.base = run.u;
+                ++run.n;
+            }
+        }
+        return true;
+    }
+    return false;
+}
 
-// A warp's ring of stages and its copies.  Step i of the segment covers tokens
-// begin + (i kAttnWarps + warp) KW + 0 .. KW-1.  A stage holds KW rows of k,
-// then KW of v, rows of RB bytes with their 16-byte pieces permuted by the row
-// (piece p of row r at p ^ key(r)), so that eight rows' equal pieces lie in
-// different banks.  Rows without a token are zeros: their v must not be
-// whatever the memory held, since 0 times NaN is NaN.
-template <int KW, int RB>
+// A warp's ring of stages and its copies.  Step i of a segment covers tokens
+// begin + (i kAttnWarps + warp) KW + 0 .. KW-1; steps are taken segment by
+// segment over the block's whole run.  A stage holds KW rows of k, then KW of
+// v, rows of RB bytes with their 16-byte pieces permuted by the row (piece p
+// of row r at p ^ key(r)), so that eight rows' equal pieces lie in different
+// banks.  Rows without a token are zeros: their v must not be whatever the
+// memory held, since 0 times NaN is NaN.
+template <int KW, int RB, bool SOLO>
 struct Ring {
     static constexpr int kPieces = RB / 16;
     static constexpr int kHalf = KW * RB, kStage = 2 * kHalf;
     static constexpr int kBytes = kStages * kStage;
-    const PagedView &c;
-    const Segment &sg;
+    static constexpr int kStep = kAttnWarps * KW;
+    const AttnArgs &a;
     uint32_t base;  // this warp's stages
-    int warp, lane, steps;
-    uint32_t live[kStages];  // which of a stage's rows hold a token
-    unsigned int *status;
+    int warp, lane;
+    Run run;        // what is left to copy behind the present segment
+    int n, h, at_tok, end;  // the present segment: the warp's next token, the segment's end
+    int steps;              // the segment's steps left
+    bool more;              // there is a step to look up
+    // the step that is issued next: has it been looked up, and row lane % KW's place
+    bool ready;
+    long long off;
+    uint32_t live[kStages - 1];  // rows that hold a token, of the steps in flight, oldest first
 
     __device__ __forceinline__ static int key(int r) { return kPieces >= 8 ? r & 7 : (r >> 1) & (kPieces - 1); }
     __device__ __forceinline__ static uint32_t at(int r, int piece) { return (uint32_t)(r * RB + ((piece ^ key(r)) << 4)); }
 
-    // the pool offset of row `lane % KW` of step i, -1 where it holds no token
-    __device__ __forceinline__ long long lookup(int i) const {
-        const int j = sg.begin + (i * kAttnWarps + warp) * KW + lane % KW;
-        if (i >= steps || j >= sg.end) return -1;
-        int entry, slot;
-        page_slot(c, j, entry, slot);
-        const int page = page_of(c, sg.n, entry);
-        if (page < 0) {
-            record_status(status, GDN2_ERR_INVALID_ARG);
-            return -1;
+    __device__ __forceinline__ void open() {
+        Segment sg;
+        steps = 0;
+        more = false;
+        while (steps == 0 && next_segment<SOLO>(a, run, sg)) {
+            n = sg.n;
+            h = sg.h;
+            at_tok = sg.begin + warp * KW;
+            end = sg.end;
+            steps = (sg.end - sg.begin + kStep - 1) / kStep;
+            more = steps > 0;
         }
-        return row_off(c, page, slot, sg.h);
     }
-    // starts step i's copies (a group of its own, empty past the last step)
-    __device__ __forceinline__ void issue(int i, int stage, long long off) {
+    // finds the rows of the next step
+    __device__ __forceinline__ void lookup() {
+        ready = more;
+        off = -1;
+        if (!more) return;
+        const int j = at_tok + lane % KW;
+        if (j < end) {
+            int entry, slot;
+            page_slot(a.c, j, entry, slot);
+            const int page = page_of(a.c, n, entry);
+            if (page >= 0) off = row_off(a.c, page, slot, h);
+            else record_status(a.status, GDN2_ERR_INVALID_ARG);
+        }
+        at_tok += kStep;
+        if (--steps == 0) open();
+    }
+    // starts the copies of the step that was looked up (a group of its own,
+    // empty past the last), and looks the one behind it up
+    __device__ __forceinline__ uint32_t issue(int stage) {
         const uint32_t ok = __ballot_sync(0xffffffffu, off >= 0);
-        live[stage] = ok;
-        if (i < steps) {
+        if (ready) {
             const uint32_t s = base + stage * kStage;
-            constexpr int kRowsAtOnce = 32 / kPieces > KW ? KW : 32 / kPieces;  // rows of one instruction
-            static_assert(KW * kPieces % 32 == 0, "whole warps of pieces");
+            constexpr int kRowsAtOnce = 32 / kPieces;  // rows of one instruction
+            static_assert(kPieces <= 32 && KW * kPieces % 32 == 0, "whole warps of pieces");
 #pragma unroll
             for (int x = 0; x < KW * kPieces / 32; ++x) {
                 const int r = x * kRowsAtOnce + lane / kPieces, piece = lane % kPieces;
                 const long long ro = __shfl_sync(0xffffffffu, off, r);
                 const long long from = (ro < 0 ? 0 : ro) + piece * 16;
-                cp_async16_zfill(s + at(r, piece), c.k + from, ro >= 0);
-                cp_async16_zfill(s + kHalf + at(r, piece), c.v + from, ro >= 0);
+                cp_async16_zfill(s + at(r, piece), a.c.k + from, ro >= 0);
+                cp_async16_zfill(s + kHalf + at(r, piece), a.c.v + from, ro >= 0);
             }
         }
         tc::cp_async_commit();
+        lookup();
+        return ok;
     }
 };
 
-// ---- bf16: products on the tensor cores, the query heads as the 16 rows.  Of
-// the instruction's rows only the group's are used; at a few flops a byte the
-// rest costs nothing that is missed.
-template <int D>
+// where channel ch of row `row` lies in a warp's merge area [rows][D]: banks
+// differ between the rows that a warp writes at once
+template <int D> __device__ __forceinline__ int merge_at(int row, int ch) { return row * D + (ch ^ ((row >> 1 & 3) << 3)); }
+
+// ---- bf16: products on the tensor cores, tokens (scores) and channels
+// (values) as the 16 rows and the query heads as NT times 8 columns:
+//   S^T [16 tokens x heads] = K Q^T,  acc^T [channels x heads] += V^T P^T.
+// A mask, a maximum and a scale factor then belong to a column, which four
+// registers of a thread share, and P^T turns from a result into an operand by
+// transposing 8 x 8 blocks between registers.
+template <int D, int NT>
 struct EngineBf16 {
     using E = __nv_bfloat16;
-    static constexpr int KW = 16, RB = 2 * D, kRows = 16;
-    uint32_t qf[D / 16][4];
-    float acc[D / 8][4];
-    float m[2], l[2];
+    static constexpr int KW = 16, RB = 2 * D, kRows = 8 * NT, kBlocksPerSm = D == 128 ? 2 : 4;
+    uint32_t qf[NT][D / 16][2];
+    float acc[NT][D / 16][4];
+    float m[NT][2], l[NT][2];
 
     __device__ __forceinline__ void begin(const AttnArgs &a, const Segment &sg, int lane, float *) {
         const E *q = static_cast<const E *>(a.q) + ((size_t)sg.n * a.H + sg.head) * D;
         const int g = lane >> 2, t = lane & 3;
 #pragma unroll
-        for (int s = 0; s < D / 16; ++s)
+        for (int i = 0; i < NT; ++i) {
+            const int row = 8 * i + g;
 #pragma unroll
-            for (int x = 0; x < 4; ++x) {
-                const int row = g + (x & 1) * 8, col = s * 16 + (x >> 1) * 8 + 2 * t;
-                qf[s][x] = row < sg.rows ? *reinterpret_cast<const uint32_t *>(q + row * D + col) : 0u;
+            for (int x = 0; x < D / 16; ++x) {
+#pragma unroll
+                for (int y = 0; y < 2; ++y)
+                    qf[i][x][y] = row < sg.rows ? *reinterpret_cast<const uint32_t *>(q + row * D + x * 16 + y * 8 + 2 * t) : 0u;
+                acc[i][x][0] = acc[i][x][1] = acc[i][x][2] = acc[i][x][3] = 0.f;
             }
-#pragma unroll
-        for (int i = 0; i < D / 8; ++i) acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.f;
-        m[0] = m[1] = -INFINITY;
-        l[0] = l[1] = 0.f;
+            m[i][0] = m[i][1] = -INFINITY;
+            l[i][0] = l[i][1] = 0.f;
+        }
     }
-    // one step of 16 tokens; `scores`: this step's place for rows of kUnit scores, or nullptr
+    // one step of 16 tokens; `scores`: this step's place in rows of kUnit scores, or nullptr
+    template <class R>
     __device__ __forceinline__ void step(const AttnArgs &a, const Segment &sg, uint32_t ks, uint32_t vs, uint32_t live,
                                          int lane, float *scores, float *) {
-        using R = Ring<KW, RB>;
-        float s[2][4] = {};
-        const int mi = lane >> 3, lr = lane & 7, t = lane & 3;
+        float s[NT][4];
+        const int mi = lane >> 3, lr = lane & 7, g = lane >> 2, t = lane & 3;
+#pragma unroll
+        for (int i = 0; i < NT; ++i) s[i][0] = s[i][1] = s[i][2] = s[i][3] = 0.f;
 #pragma unroll
         for (int x = 0; x < D / 16; ++x) {
-            uint32_t b[4];  // tokens 0..7: k pieces 2x, 2x+1; tokens 8..15: the same
-            ldmatrix4(ks + R::at((mi >> 1) * 8 + lr, 2 * x + (mi & 1)), b);
-            mma16816(s[0], qf[x], b[0], b[1]);
-            mma16816(s[1], qf[x], b[2], b[3]);
+            uint32_t k[4];
+            ldmatrix4(ks + R::at((mi & 1) * 8 + lr, 2 * x + (mi >> 1)), k);
+#pragma unroll
+            for (int i = 0; i < NT; ++i) mma16816(s[i], k, qf[i][x][0], qf[i][x][1]);
         }
+        const bool on[2] = {(live >> g & 1u) != 0, (live >> (g + 8) & 1u) != 0};
+        float mn[NT][2];
+        bool raised = false;
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
-#pragma unroll
-            for (int x = 0; x < 4; ++x) s[i][x] *= a.scale2;
-        if ((live & 0xffffu) != 0xffffu) {
-#pragma unroll
-            for (int i = 0; i < 2; ++i)
-#pragma unroll
-                for (int x = 0; x < 4; ++x)
-                    if (!(live >> (i * 8 + 2 * t + (x & 1)) & 1u)) s[i][x] = -INFINITY;
-        }
-        if (scores) {
-            const int g = lane >> 2;
-#pragma unroll
-            for (int y = 0; y < 2; ++y)
-                if (g + y * 8 < sg.rows)
-#pragma unroll
-                    for (int i = 0; i < 2; ++i)
-                        *reinterpret_cast<float2 *>(scores + (g + y * 8) * kUnit + i * 8 + 2 * t) =
-                            make_float2(s[i][2 * y], s[i][2 * y + 1]);
-        }
-        float mx[2], mn[2];
-#pragma unroll
-        for (int y = 0; y < 2; ++y) {
-            mx[y] = fmaxf(fmaxf(s[0][2 * y], s[0][2 * y + 1]), fmaxf(s[1][2 * y], s[1][2 * y + 1]));
-            mx[y] = fmaxf(mx[y], __shfl_xor_sync(0xffffffffu, mx[y], 1));
-            mx[y] = fmaxf(mx[y], __shfl_xor_sync(0xffffffffu, mx[y], 2));
-            mn[y] = fmaxf(m[y], mx[y]);
-        }
-        if (__any_sync(0xffffffffu, mn[0] > m[0] || mn[1] > m[1])) {
+        for (int i = 0; i < NT; ++i)
 #pragma unroll
             for (int y = 0; y < 2; ++y) {
-                const float f = mn[y] == m[y] ? 1.f : exp2f(m[y] - mn[y]);  // -inf - -inf is not a number
-                m[y] = mn[y];
-                l[y] *= f;
 #pragma unroll
-                for (int i = 0; i < D / 8; ++i) {
-                    acc[i][2 * y] *= f;
-                    acc[i][2 * y + 1] *= f;
-                }
+                for (int x = 0; x < 2; ++x) s[i][2 * x + y] = on[x] ? s[i][2 * x + y] * a.scale2 : -INFINITY;
+                float mx = fmaxf(s[i][y], s[i][2 + y]);
+                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
+                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
+                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
+                mn[i][y] = fmaxf(m[i][y], mx);
+                raised |= mn[i][y] > m[i][y];
             }
+        if (scores) {
+#pragma unroll
+            for (int i = 0; i < NT; ++i)
+#pragma unroll
+                for (int y = 0; y < 2; ++y)
+                    if (8 * i + 2 * t + y < sg.rows) {
+                        scores[(8 * i + 2 * t + y) * kUnit + g] = s[i][y];
+                        scores[(8 * i + 2 * t + y) * kUnit + g + 8] = s[i][2 + y];
+                    }
         }
-        uint32_t p[4];
+        if (__any_sync(0xffffffffu, raised)) {
 #pragma unroll
-        for (int y = 0; y < 2; ++y) {
-            const float ref = m[y] == -INFINITY ? 0.f : m[y];
-            float e[2][2];
+            for (int i = 0; i < NT; ++i)
 #pragma unroll
-            for (int i = 0; i < 2; ++i)
+                for (int y = 0; y < 2; ++y) {
+                    const float f = mn[i][y] == m[i][y] ? 1.f : exp2f(m[i][y] - mn[i][y]);  // -inf less -inf is no number
+                    m[i][y] = mn[i][y];
+                    l[i][y] *= f;
 #pragma unroll
-                for (int x = 0; x < 2; ++x) {
-                    e[i][x] = exp2f(s[i][2 * y + x] - ref);
-                    l[y] += e[i][x];
+                    for (int x = 0; x < D / 16; ++x) {
+                        acc[i][x][y] *= f;
+                        acc[i][x][2 + y] *= f;
+                    }
                 }
+        }
+        uint32_t p[NT][2];
+#pragma unroll
+        for (int i = 0; i < NT; ++i) {
+#pragma unroll
+            for (int y = 0; y < 2; ++y) {
+                const float ref = m[i][y] == -INFINITY ? 0.f : m[i][y];
+                s[i][y] = exp2f(s[i][y] - ref);
+                s[i][2 + y] = exp2f(s[i][2 + y] - ref);
+                l[i][y] += s[i][y] + s[i][2 + y];
+            }
             // the only rounding on the way: weights in [0, 1] to bf16, the type of
             // the v that they multiply; the sum takes them unrounded
-            p[y] = tc::pack_bf16(e[0][0], e[0][1]);
-            p[2 + y] = tc::pack_bf16(e[1][0], e[1][1]);
+            p[i][0] = transpose8x8(tc::pack_bf16(s[i][0], s[i][1]));
+            p[i][1] = transpose8x8(tc::pack_bf16(s[i][2], s[i][3]));
         }
 #pragma unroll
         for (int x = 0; x < D / 16; ++x) {
-            uint32_t b[4];  // channels 16x..+7 and +8..+15, tokens 0..7 and 8..15
-            ldmatrix4_trans(vs + R::at((mi & 1) * 8 + lr, 2 * x + (mi >> 1)), b);
-            mma16816(acc[2 * x], p, b[0], b[1]);
-            mma16816(acc[2 * x + 1], p, b[2], b[3]);
+            uint32_t v[4];
+            ldmatrix4_trans(vs + R::at((mi >> 1) * 8 + lr, 2 * x + (mi & 1)), v);
+#pragma unroll
+            for (int i = 0; i < NT; ++i) mma16816(acc[i][x], v, p[i][0], p[i][1]);
         }
     }
-    // this warp's m, l [kRows] and acc [kRows][D + 8] to shared memory
+    // this warp's m, l [kRows] and acc [kRows][D] to shared memory
     __device__ __forceinline__ void finish(float2 *ml, float *out, int lane) {
         const int g = lane >> 2, t = lane & 3;
 #pragma unroll
-        for (int y = 0; y < 2; ++y) {
-            l[y] += __shfl_xor_sync(0xffffffffu, l[y], 1);
-            l[y] += __shfl_xor_sync(0xffffffffu, l[y], 2);
-            if (t == 0) ml[g + 8 * y] = make_float2(m[y], l[y]);
+        for (int i = 0; i < NT; ++i)
 #pragma unroll
-            for (int i = 0; i < D / 8; ++i)
-                *reinterpret_cast<float2 *>(out + (g + 8 * y) * (D + 8) + i * 8 + 2 * t) =
-                    make_float2(acc[i][2 * y], acc[i][2 * y + 1]);
-        }
+            for (int y = 0; y < 2; ++y) {
+                const int row = 8 * i + 2 * t + y;
+#pragma unroll
+                for (int d = 4; d < 32; d <<= 1) l[i][y] += __shfl_xor_sync(0xffffffffu, l[i][y], d);
+                if (g == 0) ml[row] = make_float2(m[i][y], l[i][y]);
+#pragma unroll
+                for (int x = 0; x < D / 16; ++x) {
+                    out[merge_at<D>(row, 16 * x + g)] = acc[i][x][y];
+                    out[merge_at<D>(row, 16 * x + g + 8)] = acc[i][x][2 + y];
+                }
+            }
     }
 };
 
@@ -347,7 +439,7 @@ struct EngineBf16 {
 template <int D, int GP>
 struct EngineF32 {
     using E = float;
-    static constexpr int KW = 8, RB = 4 * D, kRows = GP;
+    static constexpr int KW = 8, RB = 4 * D, kRows = GP, kBlocksPerSm = D == 128 || GP == 16 ? 2 : GP == 8 ? 3 : 4;
     static constexpr int kLanes = D / 4;        // lanes of one token's channels
     static constexpr int kGroups = 32 / kLanes;  // tokens at once
     float acc[GP][4];
@@ -366,10 +458,10 @@ struct EngineF32 {
             l[g] = 0.f;
         }
     }
-    // sp: [kWarps][GP][KW] behind sq
+    // sp: [kAttnWarps][GP][KW] behind sq
+    template <class R>
     __device__ __forceinline__ void step(const AttnArgs &a, const Segment &sg, uint32_t ks, uint32_t vs, uint32_t live,
                                          int lane, float *scores, float *sq) {
-        using R = Ring<KW, RB>;
         float *sp = sq + GP * D + (threadIdx.x >> 5) * GP * KW;
         const int tok = lane & 7, part = lane >> 3;
         float s[GP];
@@ -450,7 +542,7 @@ struct EngineF32 {
 #pragma unroll
                 for (int i = 0; i < 4; ++i) acc[g][i] += __shfl_xor_sync(0xffffffffu, acc[g][i], off);
             if (lane < kLanes)
-                *reinterpret_cast<float4 *>(out + g * (D + 8) + ch * 4) =
+                *reinterpret_cast<float4 *>(out + merge_at<D>(g, ch * 4)) =
                     make_float4(acc[g][0], acc[g][1], acc[g][2], acc[g][3]);
         }
     }
@@ -482,109 +574,80 @@ __device__ __forceinline__ void write_result(const AttnArgs &a, E *o, size_t hd,
     if (a.lse2) a.lse2[hd] = none ? -INFINITY : m + log2f(l);
 }
 
-// shared memory of a block: the warps' rings, or (between segments) their
-// (m, l, acc); then what the engine keeps
+// shared memory of a block: the warps' rings, then what the engine keeps
 template <class En, int D> constexpr int attn_smem() {
-    constexpr int ring = kAttnWarps * Ring<En::KW, En::RB>::kBytes;
-    constexpr int merge = kAttnWarps * En::kRows * (8 + 4 * (D + 8));
-    constexpr int own = sizeof(typename En::E) == 4 ? En::kRows * (D + kAttnWarps * En::KW) * 4 : 0;
-    return (ring > merge ? ring : merge) + own;
+    return kAttnWarps * Ring<En::KW, En::RB, false>::kBytes +
+           (sizeof(typename En::E) == 4 ? En::kRows * (D + kAttnWarps * En::KW) * 4 : 0);
 }
 
 // SOLO: block b takes run b whole (no parts, no join).
 template <class En, int D, bool SOLO>
-__global__ void __launch_bounds__(kAttnThreads, kBlocksPerSm)
+__global__ void __launch_bounds__(kAttnThreads, En::kBlocksPerSm)
 attn_split_kernel(const AttnArgs a) {
     extern __shared__ __align__(128) unsigned char smem[];
-    using R = Ring<En::KW, En::RB>;
+    __shared__ float2 s_ml[kAttnWarps][En::kRows];
+    using R = Ring<En::KW, En::RB, SOLO>;
     using E = typename En::E;
-    constexpr int kRing = kAttnWarps * R::kBytes, kMerge = kAttnWarps * En::kRows * (8 + 4 * (D + 8));
-    float *own = reinterpret_cast<float *>(smem + (kRing > kMerge ? kRing : kMerge));
+    static_assert(R::kStage >= En::kRows * D * 4, "a stage holds a warp's accumulator");
+    float *own = reinterpret_cast<float *>(smem + kAttnWarps * R::kBytes);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const PagedView &c = a.c;
     const int per = c.Hkv * a.HB;
     allow_next_launch();
+    wait_for_previous();
     Run run;
     if constexpr (SOLO) {
         run.n = blockIdx.x / per;
         run.u = 0;
         run.end = 1;
     } else run = find_run<kAttnThreads>(c, a.window, per, kMinUnits, a.status);
-    En en;
-    while (run.u < run.end) {
-        const int len = checked_len(c, run.n, a.status), first = first_token(len, a.window);
-        const int T = (len - first + kUnit - 1) / kUnit;
-        int r, t0 = 0, cnt = T;
-        if constexpr (SOLO) r = blockIdx.x - run.n * per;
-        else {
-            if (T == 0) {
-                ++run.n;
-                continue;
-            }
-            r = (int)((run.u - run.base) / T);
-            t0 = (int)((run.u - run.base) - (long long)r * T);
-            cnt = (int)(T - t0 < run.end - run.u ? T - t0 : run.end - run.u);
-        }
-        Segment sg;
-        sg.n = run.n;
-        sg.h = r / a.HB;
-        const int hb = r - sg.h * a.HB;
-        sg.head = sg.h * a.G + hb * a.hpb;
-        sg.rows = min(a.hpb, a.G - hb * a.hpb);
-        sg.begin = first + t0 * kUnit;
-        sg.end = min(len, sg.begin + cnt * kUnit);
-        sg.unit = SOLO ? (long long)blockIdx.x * ((c.cap + kUnit - 1) / kUnit) : run.u;
 
-        constexpr int kStep = kAttnWarps * En::KW;
-        R ring{c, sg, tc::smem_addr(smem) + warp * R::kBytes, warp, lane, (sg.end - sg.begin + kStep - 1) / kStep, {}, a.status};
-        long long next = ring.lookup(0);
+    R ring{a, tc::smem_addr(smem) + warp * R::kBytes, warp, lane, run};
+    ring.open();
+    ring.lookup();
 #pragma unroll
-        for (int s = 0; s < kStages - 1; ++s) {
-            const long long off = next;
-            next = ring.lookup(s + 1);
-            ring.issue(s, s, off);
-        }
+    for (int s = 0; s < kStages - 1; ++s) ring.live[s] = ring.issue(s);
+    int stage = 0;  // the oldest step in flight
+    En en;
+    Segment sg;
+    while (next_segment<SOLO>(a, run, sg)) {
         en.begin(a, sg, lane, own);
-        for (int i0 = 0; i0 < ring.steps; i0 += kStages) {
+        const int steps = (sg.end - sg.begin + R::kStep - 1) / R::kStep;
+        for (int i = 0; i < steps; ++i) {
+            const uint32_t live = ring.live[0];
 #pragma unroll
-            for (int s = 0; s < kStages; ++s) {
-                const int i = i0 + s;
-                if (i >= ring.steps) break;
-                __syncwarp();  // the stage that the next copies go to has been read
-                const long long off = next;
-                next = ring.lookup(i + kStages);
-                ring.issue(i + kStages - 1, (s + kStages - 1) % kStages, off);
-                cp_async_wait<kStages - 1>();
-                __syncwarp();
-                const int tok = (i * kAttnWarps + warp) * En::KW;  // in the segment
-                float *sc = a.scores ? a.scores + ((sg.unit + tok / kUnit) * a.hpb) * kUnit + tok % kUnit : nullptr;
-                const uint32_t st = ring.base + s * R::kStage;
-                if (ring.live[s]) en.step(a, sg, st, st + R::kHalf, ring.live[s], lane, sc, own);
-            }
+            for (int s = 0; s + 1 < kStages - 1; ++s) ring.live[s] = ring.live[s + 1];
+            __syncwarp();  // the stage that the next copies go to has been read
+            ring.live[kStages - 2] = ring.issue(stage == 0 ? kStages - 1 : stage - 1);
+            cp_async_wait<kStages - 1>();
+            __syncwarp();
+            const int tok = (i * kAttnWarps + warp) * En::KW;  // in the segment
+            float *sc = a.scores ? a.scores + ((sg.unit + tok / kUnit) * a.hpb) * kUnit + tok % kUnit : nullptr;
+            const uint32_t st = ring.base + stage * R::kStage;
+            if (live) en.template step<R>(a, sg, st, st + R::kHalf, live, lane, sc, own);
+            stage = stage == kStages - 1 ? 0 : stage + 1;
         }
-        cp_async_wait<0>();
-        __syncthreads();  // every warp is done with its ring
-        float2 *ml = reinterpret_cast<float2 *>(smem);
-        float *po = reinterpret_cast<float *>(smem + kAttnWarps * En::kRows * 8);
-        en.finish(ml + warp * En::kRows, po + warp * En::kRows * (D + 8), lane);
+        // the stage before the oldest in flight is free: the accumulators go there
+        float *area = reinterpret_cast<float *>(smem + (stage == 0 ? kStages - 1 : stage - 1) * R::kStage);
+        __syncwarp();
+        en.finish(s_ml[warp], area + warp * (R::kBytes / 4), lane);
         __syncthreads();
-        const bool whole = SOLO || (t0 == 0 && cnt == T);
-        const int slot = 2 * blockIdx.x + (t0 == 0);
+        const int slot = 2 * blockIdx.x + sg.starts;
         for (int x = tid; x < sg.rows * (D / 4); x += kAttnThreads) {
             const int row = x / (D / 4), ch = (x - row * (D / 4)) * 4;
             float m = -INFINITY, l = 0.f;
 #pragma unroll
-            for (int w = 0; w < kAttnWarps; ++w) m = fmaxf(m, ml[w * En::kRows + row].x);
+            for (int w = 0; w < kAttnWarps; ++w) m = fmaxf(m, s_ml[w][row].x);
             float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
             for (int w = 0; w < kAttnWarps; ++w) {
-                const float2 y = ml[w * En::kRows + row];
+                const float2 y = s_ml[w][row];
                 const float f = part_factor(y, m);
-                const float4 v = *reinterpret_cast<const float4 *>(po + (w * En::kRows + row) * (D + 8) + ch);
+                const float4 v = *reinterpret_cast<const float4 *>(area + w * (R::kBytes / 4) + merge_at<D>(row, ch));
                 l += f * y.y;
                 o.x += f * v.x; o.y += f * v.y; o.z += f * v.z; o.w += f * v.w;
             }
-            if (whole) {
+            if (sg.whole) {
                 const size_t hd = (size_t)sg.n * a.H + sg.head + row;
                 write_result(a, static_cast<E *>(a.o) + hd * D + ch, hd, ch == 0, m, l, o);
             } else {
@@ -592,30 +655,26 @@ attn_split_kernel(const AttnArgs a) {
                 if (ch == 0) a.ml[(size_t)slot * kHeadBlock + row] = make_float2(m, l);
             }
         }
-        if constexpr (SOLO) return;
-        if (tid == 0 && t0 == 0)
-            a.parts[(size_t)sg.n * per + r] =
-                whole ? make_int2(-1, -1)
-                      : make_int2((int)blockIdx.x, (int)((run.base + (long long)(r + 1) * T - 1) / run.share));
-        __syncthreads();  // the merge area is the rings' again
-        run.u += cnt;
-        if (run.u == run.base + (long long)per * T) {
-            run.base = run.u;
-            ++run.n;
+        if constexpr (!SOLO) {
+            if (tid == 0 && sg.starts)
+                a.parts[(size_t)sg.n * per + sg.run] =
+                    sg.whole ? make_int2(-1, -1) : make_int2((int)blockIdx.x, (int)((sg.run_end - 1) / run.share));
         }
+        __syncthreads();  // the area is a stage again
     }
+    cp_async_wait<0>();
 }
 
 // One block a (sequence, query head): joins its parts, or writes the empty
 // sequence's result, or (no parts: it is written already) ends.  Each of the
-// block's groups of D / 4 lanes takes every kGroups-th part, four loads ahead
-// (one sequence alone leaves a part in every block).
-constexpr int kJoinThreads = 256;
-template <typename E, int D>
-__global__ void __launch_bounds__(kJoinThreads)
+// block's groups of D / 4 lanes takes every kGroups-th part, four loads ahead.
+// One sequence alone leaves a part in every block of the GPU, and then the
+// blocks here are few and have 1024 threads (NT); otherwise 128.
+template <typename E, int D, int NT>
+__global__ void __launch_bounds__(NT)
 attn_join_kernel(const AttnArgs a) {
-    constexpr int kLanes = D / 4, kGroups = kJoinThreads / kLanes, kAhead = 4;
-    __shared__ float s_m[kJoinThreads / 32];
+    constexpr int kLanes = D / 4, kGroups = NT / kLanes, kAhead = 4;
+    __shared__ float s_m[NT / 32];
     __shared__ float s_l[kGroups];
     __shared__ float4 s_o[kGroups][kLanes];
     const int tid = threadIdx.x, n = blockIdx.x / a.H, h = blockIdx.x - n * a.H, kvh = h / a.G, g = h - kvh * a.G;
@@ -644,13 +703,13 @@ attn_join_kernel(const AttnArgs a) {
         if (b <= pr.y) v[i] = *reinterpret_cast<const float4 *>(a.part + slot(b) * D + ch * 4);
     }
     float m = -INFINITY;
-    for (int b = pr.x + tid; b <= pr.y; b += kJoinThreads) m = fmaxf(m, a.ml[slot(b)].x);
+    for (int b = pr.x + tid; b <= pr.y; b += NT) m = fmaxf(m, a.ml[slot(b)].x);
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
     if ((tid & 31) == 0) s_m[tid >> 5] = m;
     __syncthreads();
 #pragma unroll
-    for (int w = 0; w < kJoinThreads / 32; ++w) m = fmaxf(m, s_m[w]);
+    for (int w = 0; w < NT / 32; ++w) m = fmaxf(m, s_m[w]);
     float l = 0.f;
     float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
     for (int b0 = pr.x + grp; b0 <= pr.y; b0 += kAhead * kGroups) {
@@ -691,6 +750,7 @@ constexpr int kWeightThreads = 256;
 __global__ void __launch_bounds__(kWeightThreads)
 attn_weights_kernel(const AttnArgs a, int solo) {
     const PagedView &c = a.c;
+    allow_next_launch();
     wait_for_previous();
     Run run = find_run<kWeightThreads>(c, a.window, c.Hkv, 1, a.status);
     const int half = threadIdx.x / kUnit, tok = threadIdx.x % kUnit;
@@ -744,7 +804,7 @@ static void head_blocks(const PagedView &c, int H, AttnArgs &a) {
 
 // places the workspace's regions (ws may be null: sizes only); returns its bytes
 static size_t attn_ws(const PagedView &c, AttnArgs &a, int add_weights, void *ws) {
-    const size_t slots = 2 * (size_t)kBlocksPerSm * sm_count(), runs = (size_t)c.N * c.Hkv * a.HB;
+    const size_t slots = 2 * (size_t)kMostBlocksPerSm * sm_count(), runs = (size_t)c.N * c.Hkv * a.HB;
     size_t o = 0;
     auto take = [&](size_t bytes) { const size_t at = o; o = align256(o + bytes); return static_cast<char *>(ws) + at; };
     a.ml = reinterpret_cast<float2 *>(take(slots * kHeadBlock * sizeof(float2)));
@@ -766,15 +826,20 @@ size_t attn_ws_bytes(const PagedView &c, int H, int add_weights) {
 
 template <class En, int D, bool SOLO>
 static cudaError_t attn_run_as(const AttnArgs &a, cudaStream_t s) {
+    static_assert(En::kBlocksPerSm <= kMostBlocksPerSm, "the workspace has parts for so many");
     constexpr int bytes = attn_smem<En, D>();
+    using E = typename En::E;
+    const int heads = a.c.N * a.H;
     cudaError_t e = cudaFuncSetAttribute(attn_split_kernel<En, D, SOLO>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
     if (e != cudaSuccess) return e;
-    launch_begin(K_ATTN_SPLIT, s);
-    attn_split_kernel<En, D, SOLO><<<SOLO ? a.c.N * a.c.Hkv * a.HB : kBlocksPerSm * sm_count(), kAttnThreads, bytes, s>>>(a);
-    launch_end(K_ATTN_SPLIT, s);
-    if ((e = cudaGetLastError()) != cudaSuccess) return e;
-    if (!SOLO && (e = launch_behind(K_ATTN_JOIN, attn_join_kernel<typename En::E, D>, a.c.N * a.H, kJoinThreads, 0, s, a)) != cudaSuccess)
-        return e;
+    e = launch_behind(K_ATTN_SPLIT, attn_split_kernel<En, D, SOLO>,
+                      SOLO ? a.c.N * a.c.Hkv * a.HB : En::kBlocksPerSm * sm_count(), kAttnThreads, bytes, s, a);
+    if (e != cudaSuccess) return e;
+    if (!SOLO) {
+        e = heads <= sm_count() ? launch_behind(K_ATTN_JOIN, attn_join_kernel<E, D, 1024>, heads, 1024, 0, s, a)
+                                : launch_behind(K_ATTN_JOIN, attn_join_kernel<E, D, 128>, heads, 128, 0, s, a);
+        if (e != cudaSuccess) return e;
+    }
     if (!a.scores) return cudaSuccess;
     return launch_behind(K_ATTN_WEIGHTS, attn_weights_kernel, 8 * sm_count(), kWeightThreads, 0, s, a, (int)SOLO);
 }
@@ -785,7 +850,7 @@ static cudaError_t attn_run(const AttnArgs &a, cudaStream_t s) {
 
 template <int D>
 static cudaError_t attn_for_d(const AttnArgs &a, cudaStream_t s) {
-    if (a.c.es == 2) return attn_run<EngineBf16<D>, D>(a, s);
+    if (a.c.es == 2) return a.hpb <= 8 ? attn_run<EngineBf16<D, 1>, D>(a, s) : attn_run<EngineBf16<D, 2>, D>(a, s);
     if (a.hpb == 1) return attn_run<EngineF32<D, 1>, D>(a, s);
     if (a.hpb == 2) return attn_run<EngineF32<D, 2>, D>(a, s);
     if (a.hpb <= 4) return attn_run<EngineF32<D, 4>, D>(a, s);

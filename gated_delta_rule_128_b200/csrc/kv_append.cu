@@ -30,6 +30,8 @@ kv_append_kernel(const PagedView c, const uint4 *k, const uint4 *v, const int *c
     __shared__ long long s_off[kAppTokens];  // byte offset of head 0's row, -1: not written
     __shared__ size_t s_w[kAppTokens];
     const int t0 = blockIdx.x * per, nt = min(per, T - t0), tid = threadIdx.x;
+    allow_next_launch();
+    wait_for_previous();
     if (cu && !table_ok(cu, c.N, T)) {
         if (tid == 0) record_status(status, GDN2_ERR_INVALID_ARG);
         return;
@@ -83,6 +85,8 @@ kv_append_kernel(const PagedView c, const uint4 *k, const uint4 *v, const int *c
 // copy above still reads the old ones).
 __global__ void __launch_bounds__(1024)
 kv_lens_kernel(const PagedView c, const int *cu, int T, int *lens_out, unsigned int *status) {
+    allow_next_launch();
+    wait_for_previous();
     const bool ok = table_ok(cu, c.N, T);
     if (!ok && threadIdx.x == 0) record_status(status, GDN2_ERR_INVALID_ARG);
     for (int n = threadIdx.x; n < c.N; n += blockDim.x) {
@@ -98,19 +102,12 @@ cudaError_t kv_append_launch(const PagedView &c, const void *k, const void *v, c
     if (T > 0) {
         const int want = T / (4 * sm_count());
         const int per = want < 1 ? 1 : (want > kAppTokens ? kAppTokens : want);
-        launch_begin(K_KV_APPEND, s);
-        kv_append_kernel<<<(T + per - 1) / per, kAppThreads, 0, s>>>(
-            c, static_cast<const uint4 *>(k), static_cast<const uint4 *>(v), cu, T, per, lens_out, status);
-        launch_end(K_KV_APPEND, s);
-        cudaError_t e = cudaGetLastError();
+        const cudaError_t e = launch_behind(K_KV_APPEND, kv_append_kernel, (T + per - 1) / per, kAppThreads, 0, s, c,
+                                            static_cast<const uint4 *>(k), static_cast<const uint4 *>(v), cu, T, per,
+                                            lens_out, status);
         if (e != cudaSuccess) return e;
     }
-    if (cu) {
-        launch_begin(K_KV_LENS, s);
-        kv_lens_kernel<<<1, 1024, 0, s>>>(c, cu, T, lens_out, status);
-        launch_end(K_KV_LENS, s);
-    }
-    return cudaGetLastError();
+    return cu ? launch_behind(K_KV_LENS, kv_lens_kernel, 1, 1024, 0, s, c, cu, T, lens_out, status) : cudaSuccess;
 }
 
 }  // namespace gdn2

@@ -22,7 +22,7 @@ namespace cg = cooperative_groups;
 
 namespace gdn2 {
 
-constexpr int kSelThreads = 1024;
+constexpr int kSelThreads = 512;
 constexpr int kSelWarps = kSelThreads / 32;
 constexpr int kBins = 2048;
 constexpr int kDigits = 3;
@@ -61,9 +61,9 @@ __device__ __forceinline__ int block_scan(int x, int *warp_tot) {
     }
     if (lane == 31) warp_tot[warp] = x;
     __syncthreads();
-    int t = warp_tot[lane];
+    int t = lane < kSelWarps ? warp_tot[lane] : 0;
 #pragma unroll
-    for (int off = 1; off < 32; off <<= 1) {
+    for (int off = 1; off < kSelWarps; off <<= 1) {
         const int y = __shfl_up_sync(0xffffffffu, t, off);
         if (lane >= off) t += y;
     }
@@ -78,7 +78,8 @@ __global__ void __launch_bounds__(kSelThreads)
 evict_select_kernel(const PagedView c, const PagedView to, int in_place, int budget, int sink, int recent,
                     int slots, int stride, int *list_all, EvictPlan *plan, unsigned int *status) {
     extern __shared__ unsigned s_key[];
-    __shared__ int hist[kDigits][kBins], warp_tot[32], s_digit, s_above;
+    __shared__ __align__(16) int hist[kDigits][kBins];
+    __shared__ int warp_tot[32], s_digit, s_above;
     __shared__ int2 s_warp[kSelWarps];  // kept for certain, equal to the threshold: a warp's
     __shared__ int2 s_block;            // the block's
     __shared__ int s_first;
@@ -88,6 +89,7 @@ evict_select_kernel(const PagedView c, const PagedView to, int in_place, int bud
     const int nh = blockIdx.x / ranks, n = nh / c.Hkv, h = nh - n * c.Hkv;
     int *list = list_all + (size_t)nh * stride;
     allow_next_launch();
+    wait_for_previous();
     const int raw = c.lens[n];
     int len = checked_len(c, n, status);
     if (min(len, budget) > to.cap) {
@@ -111,9 +113,26 @@ evict_select_kernel(const PagedView c, const PagedView to, int in_place, int bud
     auto key = [&](int j) { return held ? s_key[j - a] : key_at(c, n, h, j, status); };
     for (int x = tid; x < kDigits * kBins; x += kSelThreads) (&hist[0][0])[x] = 0;
     if (tid == 0) s_first = len;
-    if (held) {
-#pragma unroll 8
-        for (int j = a + tid; j < b; j += kSelThreads) s_key[j - a] = key_at(c, n, h, j, status);
+    if (held) {  // eight at a time, each load before any is used
+        constexpr int kAhead = 8;
+        for (int j0 = a + tid; j0 < b; j0 += kAhead * kSelThreads) {
+            int page[kAhead], slot[kAhead];
+            float w[kAhead];
+#pragma unroll
+            for (int u = 0; u < kAhead; ++u) {
+                const int j = min(j0 + u * kSelThreads, b - 1);
+                int entry;
+                page_slot(c, j, entry, slot[u]);
+                page[u] = page_of(c, n, entry);
+            }
+#pragma unroll
+            for (int u = 0; u < kAhead; ++u) w[u] = page[u] < 0 ? __uint_as_float(0x7fc00000u) : c.w[weight_off(c, page[u], slot[u], h)];
+#pragma unroll
+            for (int u = 0; u < kAhead; ++u) {
+                if (page[u] < 0) record_status(status, GDN2_ERR_INVALID_ARG);
+                if (j0 + u * kSelThreads < b) s_key[j0 + u * kSelThreads - a] = weight_key(w[u]);
+            }
+        }
     }
     __syncthreads();
     unsigned prefix = 0, mask = 0;
@@ -126,18 +145,23 @@ evict_select_kernel(const PagedView c, const PagedView to, int in_place, int bud
             if ((k & mask) == prefix) atomicAdd(&hist[d][(k >> shift) & ((1u << width) - 1)], 1);
         }
         cluster.sync();
-        // thread t: the t-th pair of digits from the top
-        const int top = kBins - 1 - 2 * tid;
-        int c1 = 0, c0 = 0;
+        // thread t: the t-th four digits from the top
+        static_assert(kBins == 4 * kSelThreads, "four bins a thread");
+        const int top = kBins - 1 - 4 * tid;
+        int4 x = make_int4(0, 0, 0, 0);
         for (int r = 0; r < ranks; ++r) {
-            const int2 x = *reinterpret_cast<const int2 *>(cluster.map_shared_rank(&hist[d][top - 1], r));
-            c0 += x.x;
-            c1 += x.y;
+            const int4 y = *reinterpret_cast<const int4 *>(cluster.map_shared_rank(&hist[d][top - 3], r));
+            x.x += y.x; x.y += y.y; x.z += y.z; x.w += y.w;
         }
-        const int inc = block_scan(c0 + c1, warp_tot), above = inc - c0 - c1;
-        if (above < need && need <= inc) {
-            s_digit = above + c1 >= need ? top : top - 1;
-            s_above = above + c1 >= need ? above : above + c1;
+        const int inc = block_scan(x.x + x.y + x.z + x.w, warp_tot);
+        int above = inc - x.x - x.y - x.z - x.w;
+        if (above < need && need <= inc) {  // one thread
+            int digit = top;
+            if (above + x.w < need) { above += x.w; --digit;
+                if (above + x.z < need) { above += x.z; --digit;
+                    if (above + x.y < need) { above += x.y; --digit; } } }
+            s_digit = digit;
+            s_above = above;
         }
         __syncthreads();
         prefix |= (unsigned)s_digit << shift;
@@ -196,54 +220,88 @@ evict_select_kernel(const PagedView c, const PagedView to, int in_place, int bud
     cluster.sync();  // no block ends while another reads its memory
 }
 
-// Into another cache: the kept rows in any order.  A block carries kRows rows
-// of one (sequence, head) at a time, k and v, a thread the same 16-byte piece
-// of kDeep rows of each.
+// Into another cache: the kept rows in any order.  An item is a chunk of rows
+// of one (sequence, head), a thread carrying the same 16-byte piece of kDeep
+// rows of k and of v; the next item's places are looked up (list, then tables)
+// while this one's rows are on their way.  The weights are items of their own.
 constexpr int kDeep = 4;
-__global__ void __launch_bounds__(kMoveThreads)
-evict_copy_kernel(const PagedView c, const PagedView to, int stride, int chunks, const int *list_all,
+constexpr int kCopyBlocksPerSm = 3;
+__global__ void __launch_bounds__(kMoveThreads, kCopyBlocksPerSm)
+evict_copy_kernel(const PagedView c, const PagedView to, int stride, int chunks, int wchunks, const int *list_all,
                   const EvictPlan *plan, unsigned int *status) {
     const int pieces = c.d * c.es / 16, at_once = kMoveThreads / pieces;
     const int piece = threadIdx.x % pieces, r = threadIdx.x / pieces;
-    const long long total = (long long)c.N * c.Hkv * chunks;
+    const long long rows = (long long)c.N * c.Hkv * chunks, total = rows + (long long)c.N * c.Hkv * wchunks;
+    long long from[kDeep], dst[kDeep];
+    allow_next_launch();
     wait_for_previous();
-    for (long long x = blockIdx.x; x < total; x += gridDim.x) {
-        const int nh = (int)(x / chunks), chunk = (int)(x - (long long)nh * chunks);
+    // the places of row i0 + u step, u < kDeep, of (sequence, head) nh; -1: not written
+    auto places = [&](int nh, long long i0, int step, auto place) {
         const int n = nh / c.Hkv, h = nh - n * c.Hkv, count = plan[nh].count;
         const int *list = list_all + (size_t)nh * stride;
-        const long long i0 = (long long)chunk * at_once * kDeep + r;
+        int src[kDeep], page[kDeep], page2[kDeep], slot[kDeep], slot2[kDeep];
+#pragma unroll
+        for (int u = 0; u < kDeep; ++u) src[u] = i0 + u * step < count ? list[i0 + u * step] : -1;
+#pragma unroll
+        for (int u = 0; u < kDeep; ++u) {
+            page[u] = page2[u] = -1;
+            if (src[u] < 0) continue;
+            int entry, entry2;
+            page_slot(c, src[u], entry, slot[u]);
+            page_slot(to, (int)(i0 + u * step), entry2, slot2[u]);
+            page[u] = page_of(c, n, entry);
+            page2[u] = page_of(to, n, entry2);
+        }
+#pragma unroll
+        for (int u = 0; u < kDeep; ++u) {
+            const bool ok = page[u] >= 0 && page2[u] >= 0;
+            if (src[u] >= 0 && !ok) record_status(status, GDN2_ERR_INVALID_ARG);
+            from[u] = dst[u] = -1;
+            if (ok) place(u, page[u], slot[u], page2[u], slot2[u], h);
+        }
+    };
+    auto row_places = [&](long long x) {
+        const int nh = (int)(x / chunks), chunk = (int)(x - (long long)nh * chunks);
+        places(nh, (long long)chunk * at_once * kDeep + r, at_once, [&](int u, int pg, int sl, int pg2, int sl2, int h) {
+            from[u] = row_off(c, pg, sl, h) + piece * 16;
+            dst[u] = row_off(to, pg2, sl2, h) + piece * 16;
+        });
+        if (chunk == 0 && threadIdx.x == 0 && nh % c.Hkv == 0) to.lens[nh / c.Hkv] = plan[nh].count;
+    };
+    long long x = blockIdx.x;
+    if (x < rows) row_places(x);
+    for (; x < rows; x += gridDim.x) {
         uint4 k[kDeep], v[kDeep];
+        long long at[kDeep];
+#pragma unroll
+        for (int u = 0; u < kDeep; ++u) {
+            at[u] = dst[u];
+            if (at[u] < 0) continue;
+            k[u] = *reinterpret_cast<const uint4 *>(c.k + from[u]);
+            v[u] = *reinterpret_cast<const uint4 *>(c.v + from[u]);
+        }
+        if (x + gridDim.x < rows) row_places(x + gridDim.x);
+#pragma unroll
+        for (int u = 0; u < kDeep; ++u) {
+            if (at[u] < 0) continue;
+            *reinterpret_cast<uint4 *>(to.k + at[u]) = k[u];
+            *reinterpret_cast<uint4 *>(to.v + at[u]) = v[u];
+        }
+    }
+    for (; x < total; x += gridDim.x) {
+        const int nh = (int)((x - rows) / wchunks), chunk = (int)(x - rows - (long long)nh * wchunks);
+        places(nh, (long long)chunk * kMoveThreads * kDeep + threadIdx.x, kMoveThreads,
+               [&](int u, int pg, int sl, int pg2, int sl2, int h) {
+                   from[u] = (long long)weight_off(c, pg, sl, h);
+                   dst[u] = (long long)weight_off(to, pg2, sl2, h);
+               });
         float w[kDeep];
-        long long dst[kDeep];
-        size_t wd[kDeep];
 #pragma unroll
-        for (int u = 0; u < kDeep; ++u) {
-            const long long i = i0 + u * at_once;
-            dst[u] = -1;
-            if (i >= count) continue;
-            int entry, slot, entry2, slot2;
-            page_slot(c, list[i], entry, slot);
-            page_slot(to, (int)i, entry2, slot2);
-            const int page = page_of(c, n, entry), page2 = page_of(to, n, entry2);
-            if (page < 0 || page2 < 0) {
-                record_status(status, GDN2_ERR_INVALID_ARG);
-                continue;
-            }
-            const long long from = row_off(c, page, slot, h) + piece * 16;
-            k[u] = *reinterpret_cast<const uint4 *>(c.k + from);
-            v[u] = *reinterpret_cast<const uint4 *>(c.v + from);
-            if (piece == 0) w[u] = c.w[weight_off(c, page, slot, h)];
-            dst[u] = row_off(to, page2, slot2, h) + piece * 16;
-            wd[u] = weight_off(to, page2, slot2, h);
-        }
+        for (int u = 0; u < kDeep; ++u)
+            if (dst[u] >= 0) w[u] = c.w[from[u]];
 #pragma unroll
-        for (int u = 0; u < kDeep; ++u) {
-            if (dst[u] < 0) continue;
-            *reinterpret_cast<uint4 *>(to.k + dst[u]) = k[u];
-            *reinterpret_cast<uint4 *>(to.v + dst[u]) = v[u];
-            if (piece == 0) to.w[wd[u]] = w[u];
-        }
-        if (h == 0 && chunk == 0 && threadIdx.x == 0) to.lens[n] = count;
+        for (int u = 0; u < kDeep; ++u)
+            if (dst[u] >= 0) to.w[dst[u]] = w[u];
     }
 }
 
@@ -260,6 +318,7 @@ evict_shift_kernel(const PagedView c, int stride, const int *list_all, const Evi
     const int columns = c.d * c.es / (16 * LANES);
     const int nh = blockIdx.x / (2 * columns), col = blockIdx.x % (2 * columns);
     const int n = nh / c.Hkv, h = nh - n * c.Hkv;
+    allow_next_launch();
     wait_for_previous();
     const EvictPlan p = plan[nh];
     const int *list = list_all + (size_t)nh * stride;
@@ -342,20 +401,8 @@ cudaError_t evict_launch(const PagedView &src, const PagedView &dst, bool in_pla
     const int slots = (int)(((long long)src.cap + ranks - 1) / ranks < kMaxKeys ? (src.cap + ranks - 1) / ranks : kMaxKeys);
     cudaError_t e = cudaFuncSetAttribute(evict_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxKeys * 4);
     if (e != cudaSuccess) return e;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = ranks;
-    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(nh * ranks);
-    cfg.blockDim = dim3(kSelThreads);
-    cfg.dynamicSmemBytes = slots * 4;
-    cfg.stream = s;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    launch_begin(K_EVICT_SELECT, s);
-    e = cudaLaunchKernelEx(&cfg, evict_select_kernel, src, dst, (int)in_place, budget, sink, recent, slots, stride, list, plan, status);
-    launch_end(K_EVICT_SELECT, s);
+    e = launch_clusters(K_EVICT_SELECT, evict_select_kernel, ranks, nh * ranks, kSelThreads, slots * 4, s, src, dst,
+                        (int)in_place, budget, sink, recent, slots, stride, list, plan, status);
     if (e != cudaSuccess) return e;
     if (in_place) {
         const long long narrow = (long long)nh * 2 * (src.d * src.es / 16);  // blocks of 16-byte columns
@@ -364,9 +411,10 @@ cudaError_t evict_launch(const PagedView &src, const PagedView &dst, bool in_pla
         return shift_launch<1>(src, stride, list, plan, status, s);
     }
     const int rows = kMoveThreads / (src.d * src.es / 16) * kDeep, chunks = (stride + rows - 1) / rows;
-    const long long blocks = (long long)nh * chunks, most = 64LL * sm_count();
-    return launch_behind(K_EVICT_MOVE, evict_copy_kernel, (int)(blocks < most ? blocks : most), kMoveThreads, 0, s, src,
-                         dst, stride, chunks, list, plan, status);
+    const int wchunks = (stride + kMoveThreads * kDeep - 1) / (kMoveThreads * kDeep);
+    const long long items = (long long)nh * (chunks + wchunks), most = (long long)kCopyBlocksPerSm * sm_count();
+    return launch_behind(K_EVICT_MOVE, evict_copy_kernel, (int)(items < most ? items : most), kMoveThreads, 0, s, src,
+                         dst, stride, chunks, wchunks, list, plan, status);
 }
 
 }  // namespace gdn2

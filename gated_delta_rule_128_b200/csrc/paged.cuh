@@ -53,23 +53,31 @@ __device__ __forceinline__ void allow_next_launch() { asm volatile("griddepcontr
 __device__ __forceinline__ void wait_for_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
 // launches a kernel whose blocks come up while the one before it still runs
-// (they wait for it themselves)
+// (they wait for it themselves), in clusters of `ranks` blocks
 template <typename... P, typename... A>
-static cudaError_t launch_behind(int kind, void (*kernel)(P...), int grid, int threads, int smem, cudaStream_t s, A... args) {
-    cudaLaunchAttribute at[1];
+static cudaError_t launch_clusters(int kind, void (*kernel)(P...), int ranks, int grid, int threads, int smem,
+                                   cudaStream_t s, A... args) {
+    cudaLaunchAttribute at[2];
     at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     at[0].val.programmaticStreamSerializationAllowed = 1;
+    at[1].id = cudaLaunchAttributeClusterDimension;
+    at[1].val.clusterDim.x = ranks;
+    at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(grid);
     cfg.blockDim = dim3(threads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
     cfg.attrs = at;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = ranks > 1 ? 2 : 1;
     launch_begin(kind, s);
     const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, P(args)...);
     launch_end(kind, s);
     return e;
+}
+template <typename... P, typename... A>
+static cudaError_t launch_behind(int kind, void (*kernel)(P...), int grid, int threads, int smem, cudaStream_t s, A... args) {
+    return launch_clusters(kind, kernel, 1, grid, threads, smem, s, args...);
 }
 
 cudaError_t kv_append_launch(const PagedView &c, const void *k, const void *v, const int *cu, int T,
