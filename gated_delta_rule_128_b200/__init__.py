@@ -457,14 +457,6 @@ def _tensor(name: str, t: torch.Tensor, dtype, shape, device) -> None:
     raise ValueError(f"{name} must be contiguous")
 
 
-def _workspace(ws: Optional[torch.Tensor], n: int, device) -> torch.Tensor:
-    if ws is None:
-        return torch.empty(n, dtype=torch.uint8, device=device)
-    if ws.device != device or not ws.is_contiguous():
-        raise ValueError(f"ws must be contiguous, on {device}")
-    return ws
-
-
 class PagedKV:
     """A paged key-value cache: the tensors, checked once, and their C descriptor.
 
@@ -476,7 +468,7 @@ class PagedKV:
     contents may change at any time (the table and lengths are read by the
     kernels); a cache of other tensors is another object."""
 
-    __slots__ = ("k", "v", "block_table", "seq_lens", "weights", "device", "struct", "ref", "_ws_bytes")
+    __slots__ = ("k", "v", "block_table", "seq_lens", "weights", "device", "struct", "ref", "_ws_bytes", "_untouched")
 
     def __init__(self, k, v, block_table, seq_lens, weights=None):
         if k.dim() != 4 or v.shape != k.shape:
@@ -508,6 +500,7 @@ class PagedKV:
                                      N, H, d, io)
         self.ref = ctypes.byref(self.struct)
         self._ws_bytes = {}  # workspace sizes, by what they depend on
+        self._untouched = None  # a workspace for calls that use none
 
     def workspace_bytes(self, fn: str, *args) -> int:
         """The size that a call's workspace query returns for this cache."""
@@ -518,6 +511,18 @@ class PagedKV:
                 raise Gdn2Error(fn, 2)
             self._ws_bytes[(fn, args)] = n
         return n
+
+    def _workspace(self, ws, fn: str, *args) -> torch.Tensor:
+        if ws is not None:
+            if ws.device != self.device or not ws.is_contiguous():
+                raise ValueError(f"ws must be contiguous, on {self.device}")
+            return ws
+        n = self.workspace_bytes(fn, *args)
+        if n > 256:
+            return torch.empty(n, dtype=torch.uint8, device=self.device)
+        if self._untouched is None:
+            self._untouched = torch.empty(256, dtype=torch.uint8, device=self.device)
+        return self._untouched
 
 
 _HERE = contextlib.nullcontext()
@@ -581,8 +586,8 @@ def attn_decode_step(q, kv: PagedKV, *, scale: Optional[float] = None, window: i
     with _on_stream(kv, stream):
         if o is None:
             o = torch.empty_like(q)
-        lse = torch.empty((s.N, H), dtype=torch.float32, device=kv.device) if want_lse else None
-        ws = _workspace(ws, kv.workspace_bytes("gdn2_attn_decode_workspace_bytes", H, bool(add_weights)), kv.device)
+        lse = torch.empty(s.N, H, dtype=torch.float32, device=kv.device) if want_lse else None
+        ws = kv._workspace(ws, "gdn2_attn_decode_workspace_bytes", H, bool(add_weights))
         rc = lib().gdn2_attn_decode_step(kv.ref, q.data_ptr(), o.data_ptr(), None if lse is None else lse.data_ptr(),
                                          H, s.d ** -0.5 if scale is None else scale, window, bool(add_weights),
                                          ws.data_ptr(), ws.nbytes, _raw_stream(kv.device.index))
@@ -605,7 +610,7 @@ def kv_evict(kv: PagedKV, budget: int, *, sink: int = 0, recent: int = 0, dst: O
         raise ValueError(f"budget must be at least 1, got {budget}")
     with _on_stream(kv, stream):
         kept = torch.empty((s.N, s.H_kv, budget), dtype=torch.int32, device=kv.device) if want_kept else None
-        ws = _workspace(ws, kv.workspace_bytes("gdn2_kv_evict_workspace_bytes", budget), kv.device)
+        ws = kv._workspace(ws, "gdn2_kv_evict_workspace_bytes", budget)
         rc = lib().gdn2_kv_evict(kv.ref, None if dst is None else dst.ref, budget, sink, recent,
                                  None if kept is None else kept.data_ptr(), ws.data_ptr(), ws.nbytes,
                                  _raw_stream(kv.device.index))

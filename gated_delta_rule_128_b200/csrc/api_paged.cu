@@ -70,7 +70,7 @@ gdn2_status make_view(PagedView &c, const gdn2_paged_kv *kv) {
 
 gdn2_status check_heads(const PagedView &c, int H) {
     if (H < 1 || H % c.Hkv != 0) return GDN2_ERR_INVALID_ARG;
-    return (long long)c.N * H > 0x7fffffffLL / 64 ? GDN2_ERR_UNSUPPORTED : GDN2_OK;
+    return H / c.Hkv > kMaxHeadGroup || (long long)c.N * H > 0x7fffffffLL / 64 || !attn_countable(c, H) ? GDN2_ERR_UNSUPPORTED : GDN2_OK;
 }
 
 gdn2_status launched(cudaError_t e) { return e == cudaSuccess ? GDN2_OK : GDN2_ERR_CUDA; }

@@ -18,7 +18,7 @@
 //   m = max m_i,  o = sum e^(m_i - m) acc_i / sum e^(m_i - m) l_i.
 // Exponents are in base 2 throughout (scale carries log2 e).
 //
-// Within a block each warp owns 16-token (bf16) or 8-token (float32) slices of
+// Within a block each warp owns 16-token (float32, d = 128: 8-token) slices of
 // its own: it copies their k and v rows into its ring of stages in shared
 // memory with 16-byte asynchronous copies and works on them without a
 // block-wide barrier; the four warps' (m, l, acc) meet once a segment.  The
@@ -33,6 +33,7 @@ constexpr int kAttnWarps = 4;
 constexpr int kAttnThreads = 32 * kAttnWarps;
 constexpr int kUnit = 64;        // tokens of a unit
 constexpr int kMostBlocksPerSm = 4;
+constexpr int kMostGroup = kMaxHeadGroup;
 constexpr int kHeadBlock = 16;   // most query heads of one pass
 constexpr int kStages = 3;
 constexpr int kMinUnits = 2;     // fewest units worth a block of their own
@@ -65,65 +66,56 @@ __device__ __forceinline__ int units_of(const PagedView &c, int n, int window, u
     return (len - first_token(len, window) + kUnit - 1) / kUnit;
 }
 
-// The run of units of block blockIdx.x out of gridDim.x, `per` (= Hkv times
+// The run of units of block `block` out of `blocks`, `per` (= Hkv times
 // head blocks) runs of units a sequence, at least `least` units a block:
 // [u, end) and the sequence n, whose units start at `base`, that u lies in.
+// (The host refuses calls of 2^30 units or more.)
 struct Run {
-    long long u, end, share, base;
-    int n;
+    int u, end, share, base, n;
 };
 template <int NT>
-__device__ __forceinline__ Run find_run(const PagedView &c, int window, int per, int least, unsigned int *status) {
-    __shared__ long long s_warp[NT / 32], s_base;
-    __shared__ int s_n;
+__device__ __forceinline__ Run find_run(const PagedView &c, int window, int per, int least, unsigned int *status, int block,
+                                        int blocks) {
+    __shared__ int s_warp[NT / 32], s_n, s_base;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    long long x = 0, mine = 0;
+    int x = 0, mine = 0;
     for (int n = tid; n < c.N; n += NT) x += mine = units_of(c, n, window, status);
-    long long inc = x;
+    int inc = x;  // inclusive scan over the threads
+    auto scan = [&]() {
 #pragma unroll
-    for (int off = 1; off < 32; off <<= 1) {
-        const long long y = __shfl_up_sync(0xffffffffu, inc, off);
-        if (lane >= off) inc += y;
-    }
-    if (lane == 31) s_warp[warp] = inc;
-    __syncthreads();
-    long long total = 0;
+        for (int off = 1; off < 32; off <<= 1) {
+            const int y = __shfl_up_sync(0xffffffffu, inc, off);
+            if (lane >= off) inc += y;
+        }
+        if (lane == 31) s_warp[warp] = inc;
+        __syncthreads();
+        int t = lane < NT / 32 ? s_warp[lane] : 0;
+        int before = lane < warp ? t : 0;
 #pragma unroll
-    for (int i = 0; i < NT / 32; ++i) {
-        if (i < warp) inc += s_warp[i];
-        total += s_warp[i];
-    }
-    const long long all_units = total;
-    total *= per;
+        for (int off = 16; off > 0; off >>= 1) {
+            t += __shfl_xor_sync(0xffffffffu, t, off);
+            before += __shfl_xor_sync(0xffffffffu, before, off);
+        }
+        inc += before;
+        return t;  // the sum
+    };
+    int all = scan();
+    const int total = all * per;
     Run r;
-    r.share = (total + gridDim.x - 1) / gridDim.x;
-    if (r.share < least) r.share = least;
-    r.u = r.share * blockIdx.x;
-    r.end = r.u + r.share < total ? r.u + r.share : total;
+    r.share = max(least, (total + blocks - 1) / blocks);
+    r.u = r.share * block;
+    r.end = min(r.u + r.share, total);
     r.base = 0;
     r.n = 0;
     if (r.u >= total) return r;  // u >= end: nothing to do
-    long long before = 0, all = all_units;
-    for (int n0 = 0;;) {  // chunks of NT sequences; the only one's scan is the one above
+    for (int n0 = 0, before = 0;;) {  // chunks of NT sequences; the only one's scan is the one above
         if (c.N > NT) {
             inc = mine = n0 + tid < c.N ? units_of(c, n0 + tid, window, status) : 0;
-#pragma unroll
-            for (int off = 1; off < 32; off <<= 1) {
-                const long long y = __shfl_up_sync(0xffffffffu, inc, off);
-                if (lane >= off) inc += y;
-            }
             __syncthreads();  // s_warp has been read
-            if (lane == 31) s_warp[warp] = inc;
-            __syncthreads();
-            all = 0;
-#pragma unroll
-            for (int i = 0; i < NT / 32; ++i) {
-                if (i < warp) inc += s_warp[i];
-                all += s_warp[i];
-            }
+            all = scan();
         }
-        const long long lo = (before + inc - mine) * per, hi = (before + inc) * per;
-        if (lo <= r.u && r.u < hi) {
+        const int lo = (before + inc - mine) * per;
+        if (lo <= r.u && r.u < lo + mine * per) {
             s_n = n0 + tid;
             s_base = lo;
         }
@@ -169,8 +161,8 @@ struct Segment {
     int n, h, head, rows, begin, end;
     int run;             // (h, head block) in the sequence
     bool starts, whole;  // it starts at the run's first unit, and covers it
-    long long unit;      // the number of its first unit
-    long long run_end;   // one past the run's last unit
+    int unit;            // the number of its first unit
+    int run_end;         // one past the run's last unit
 };
 // the next segment of a run of units (false: there is none)
 template <bool SOLO>
@@ -183,19 +175,19 @@ __device__ __forceinline__ bool next_segment(const AttnArgs &a, Run &run, Segmen
         int t0 = 0, cnt = T;
         if constexpr (SOLO) {
             sg.run = blockIdx.x - run.n * per;
-            sg.unit = (long long)blockIdx.x * ((c.cap + kUnit - 1) / kUnit);
+            sg.unit = blockIdx.x * ((c.cap + kUnit - 1) / kUnit);
             run.u = run.end;
         } else {
             if (T == 0) {
                 ++run.n;
                 continue;
             }
-            const long long in = run.u - run.base, left = run.end - run.u;
-            sg.run = (int)(in < 0x7fffffffLL ? (unsigned)in / (unsigned)T : in / T);
-            t0 = (int)(in - (long long)sg.run * T);
-            cnt = (int)(T - t0 < left ? T - t0 : left);
+            const int in = run.u - run.base;
+            sg.run = in / T;
+            t0 = in - sg.run * T;
+            cnt = min(T - t0, run.end - run.u);
             sg.unit = run.u;
-            sg.run_end = run.base + (long long)(sg.run + 1) * T;
+            sg.run_end = run.base + (sg.run + 1) * T;
         }
         sg.n = run.n;
         sg.h = sg.run / a.HB;
@@ -208,7 +200,7 @@ __device__ __forceinline__ bool next_segment(const AttnArgs &a, Run &run, Segmen
         sg.whole = t0 == 0 && cnt == T;
         if constexpr (!SOLO) {
             run.u += cnt;
-            if (run.u == run.base + (long long)per * T) {
+            if (run.u == run.base + per * T) {
                 run.base = run.u;
                 ++run.n;
             }
@@ -238,9 +230,11 @@ struct Ring {
     int n, h, at_tok, end;  // the present segment: the warp's next token, the segment's end
     int steps;              // the segment's steps left
     bool more;              // there is a step to look up
-    // the step that is issued next: has it been looked up, and row lane % KW's place
-    bool ready;
-    long long off;
+    // the step that is issued next: whether there is one, whether row lane % KW
+    // of it holds a token, and that row's page (as the table has it, not used
+    // before the issue, so that the load does not hold anything up), slot, head
+    bool ready, token;
+    int page, slot, head;
     uint32_t live[kStages - 1];  // rows that hold a token, of the steps in flight, oldest first
 
     __device__ __forceinline__ static int key(int r) { return kPieces >= 8 ? r & 7 : (r >> 1) & (kPieces - 1); }
@@ -262,15 +256,15 @@ struct Ring {
     // finds the rows of the next step
     __device__ __forceinline__ void lookup() {
         ready = more;
-        off = -1;
+        token = false;
         if (!more) return;
         const int j = at_tok + lane % KW;
         if (j < end) {
-            int entry, slot;
+            int entry;
             page_slot(a.c, j, entry, slot);
-            const int page = page_of(a.c, n, entry);
-            if (page >= 0) off = row_off(a.c, page, slot, h);
-            else record_status(a.status, GDN2_ERR_INVALID_ARG);
+            page = __ldg(a.c.table + (size_t)n * a.c.max_pages + entry);
+            head = h;
+            token = true;
         }
         at_tok += kStep;
         if (--steps == 0) open();
@@ -278,6 +272,11 @@ struct Ring {
     // starts the copies of the step that was looked up (a group of its own,
     // empty past the last), and looks the one behind it up
     __device__ __forceinline__ uint32_t issue(int stage) {
+        long long off = -1;
+        if (token) {
+            if ((unsigned)page < (unsigned)a.c.num_pages) off = row_off(a.c, page, slot, head);
+            else record_status(a.status, GDN2_ERR_INVALID_ARG);
+        }
         const uint32_t ok = __ballot_sync(0xffffffffu, off >= 0);
         if (ready) {
             const uint32_t s = base + stage * kStage;
@@ -434,14 +433,19 @@ struct EngineBf16 {
 
 // ---- float32: products on the CUDA cores (the tensor cores' tf32 would lose
 // what a float32 cache is kept for).  Scores: lane (part, token) = (lane / 8,
-// lane % 8) sums a quarter of the channels; values: a lane owns four channels
-// of every (128 / D)-th token.  GP: query heads, padded to a power of two.
+// lane % 8) sums a quarter of the channels of KT tokens, so that a piece of q
+// is read from shared memory once for KT of them; values: a lane owns four
+// channels of every (128 / D)-th token, and reads that token's weights for four
+// heads at once.  GP: query heads, padded to a power of two.
 template <int D, int GP>
 struct EngineF32 {
     using E = float;
-    static constexpr int KW = 8, RB = 4 * D, kRows = GP, kBlocksPerSm = D == 128 || GP == 16 ? 2 : GP == 8 ? 3 : 4;
-    static constexpr int kLanes = D / 4;        // lanes of one token's channels
+    static constexpr int KT = 1;
+    static constexpr int KW = 8 * KT, RB = 4 * D, kRows = GP;
+    static constexpr int kBlocksPerSm = D == 128 || GP == 16 ? 2 : GP == 8 ? 3 : 4;
+    static constexpr int kLanes = D / 4;         // lanes of one token's channels
     static constexpr int kGroups = 32 / kLanes;  // tokens at once
+    static constexpr int kVec = GP < 4 ? GP : 4;
     float acc[GP][4];
     float m[GP], l[GP];
 
@@ -458,34 +462,43 @@ struct EngineF32 {
             l[g] = 0.f;
         }
     }
-    // sp: [kAttnWarps][GP][KW] behind sq
+    // sp: [kAttnWarps][KW][GP] behind sq
     template <class R>
     __device__ __forceinline__ void step(const AttnArgs &a, const Segment &sg, uint32_t ks, uint32_t vs, uint32_t live,
                                          int lane, float *scores, float *sq) {
         float *sp = sq + GP * D + (threadIdx.x >> 5) * GP * KW;
         const int tok = lane & 7, part = lane >> 3;
-        float s[GP];
+        float s[KT][GP];
 #pragma unroll
-        for (int g = 0; g < GP; ++g) s[g] = 0.f;
+        for (int y = 0; y < KT; ++y)
+#pragma unroll
+            for (int g = 0; g < GP; ++g) s[y][g] = 0.f;
 #pragma unroll
         for (int x = 0; x < D / 16; ++x) {
             const int piece = 4 * x + part;
-            const float4 k = ld4(ks + R::at(tok, piece));
+            float4 k[KT];
+#pragma unroll
+            for (int y = 0; y < KT; ++y) k[y] = ld4(ks + R::at(tok + 8 * y, piece));
 #pragma unroll
             for (int g = 0; g < GP; ++g) {
                 const float4 q = *reinterpret_cast<const float4 *>(sq + g * D + piece * 4);
-                s[g] = fmaf(k.x, q.x, fmaf(k.y, q.y, fmaf(k.z, q.z, fmaf(k.w, q.w, s[g]))));
+#pragma unroll
+                for (int y = 0; y < KT; ++y)
+                    s[y][g] = fmaf(k[y].x, q.x, fmaf(k[y].y, q.y, fmaf(k[y].z, q.z, fmaf(k[y].w, q.w, s[y][g]))));
             }
         }
         bool raised = false;
         float mn[GP];
-        const bool on = live >> tok & 1u;
 #pragma unroll
         for (int g = 0; g < GP; ++g) {
-            s[g] += __shfl_xor_sync(0xffffffffu, s[g], 8);
-            s[g] += __shfl_xor_sync(0xffffffffu, s[g], 16);
-            s[g] = on ? s[g] * a.scale2 : -INFINITY;
-            mn[g] = s[g];
+            mn[g] = -INFINITY;
+#pragma unroll
+            for (int y = 0; y < KT; ++y) {
+                s[y][g] += __shfl_xor_sync(0xffffffffu, s[y][g], 8);
+                s[y][g] += __shfl_xor_sync(0xffffffffu, s[y][g], 16);
+                s[y][g] = live >> (tok + 8 * y) & 1u ? s[y][g] * a.scale2 : -INFINITY;
+                mn[g] = fmaxf(mn[g], s[y][g]);
+            }
 #pragma unroll
             for (int off = 1; off < 8; off <<= 1) mn[g] = fmaxf(mn[g], __shfl_xor_sync(0xffffffffu, mn[g], off));
             mn[g] = fmaxf(m[g], mn[g]);
@@ -494,7 +507,9 @@ struct EngineF32 {
         if (scores && part == 0)
 #pragma unroll
             for (int g = 0; g < GP; ++g)
-                if (g < sg.rows) scores[g * kUnit + tok] = s[g];
+                if (g < sg.rows)
+#pragma unroll
+                    for (int y = 0; y < KT; ++y) scores[g * kUnit + tok + 8 * y] = s[y][g];
         if (raised) {  // the same on every lane: m and mn are
 #pragma unroll
             for (int g = 0; g < GP; ++g) {
@@ -508,9 +523,12 @@ struct EngineF32 {
 #pragma unroll
         for (int g = 0; g < GP; ++g) {
             if (GP >= 4 && (g & 3) != part) continue;  // shared out among the four parts
-            const float e = exp2f(s[g] - (m[g] == -INFINITY ? 0.f : m[g]));
-            l[g] += e;
-            if (GP >= 4 || part == 0) sp[g * KW + tok] = e;
+#pragma unroll
+            for (int y = 0; y < KT; ++y) {
+                const float e = exp2f(s[y][g] - (m[g] == -INFINITY ? 0.f : m[g]));
+                l[g] += e;
+                if (GP >= 4 || part == 0) sp[(tok + 8 * y) * GP + g] = e;
+            }
         }
         __syncwarp();
         const int grp = lane / kLanes, ch = lane % kLanes;
@@ -519,12 +537,22 @@ struct EngineF32 {
             const int r = x * kGroups + grp;
             const float4 v = ld4(vs + R::at(r, ch));
 #pragma unroll
-            for (int g = 0; g < GP; ++g) {
-                const float e = sp[g * KW + r];
-                acc[g][0] = fmaf(e, v.x, acc[g][0]);
-                acc[g][1] = fmaf(e, v.y, acc[g][1]);
-                acc[g][2] = fmaf(e, v.z, acc[g][2]);
-                acc[g][3] = fmaf(e, v.w, acc[g][3]);
+            for (int g0 = 0; g0 < GP; g0 += kVec) {
+                float e[kVec];
+                if constexpr (kVec == 4) {
+                    const float4 t = *reinterpret_cast<const float4 *>(sp + r * GP + g0);
+                    e[0] = t.x; e[1] = t.y; e[2] = t.z; e[3] = t.w;
+                } else {
+#pragma unroll
+                    for (int i = 0; i < kVec; ++i) e[i] = sp[r * GP + i];
+                }
+#pragma unroll
+                for (int i = 0; i < kVec; ++i) {
+                    acc[g0 + i][0] = fmaf(e[i], v.x, acc[g0 + i][0]);
+                    acc[g0 + i][1] = fmaf(e[i], v.y, acc[g0 + i][1]);
+                    acc[g0 + i][2] = fmaf(e[i], v.z, acc[g0 + i][2]);
+                    acc[g0 + i][3] = fmaf(e[i], v.w, acc[g0 + i][3]);
+                }
             }
         }
     }
@@ -563,6 +591,9 @@ __device__ __forceinline__ void store4(__nv_bfloat16 *p, float4 v) {
 __device__ __forceinline__ float part_factor(float2 y, float m) {
     return y.x == -INFINITY ? (y.y == 0.f ? 0.f : 1.f) : exp2f(y.x - m);
 }
+// the row of ml and part where block b's part of a run, in blocks pr.x .. pr.y,
+// has head `row`: the block where the run begins has it second, the others first
+__device__ __forceinline__ size_t part_row(int2 pr, int b, int row) { return (size_t)(2 * b + (b == pr.x)) * kHeadBlock + row; }
 // four channels of o, and (first: once a head) the log-sum-exp
 template <typename E>
 __device__ __forceinline__ void write_result(const AttnArgs &a, E *o, size_t hd, bool first, float m, float l, float4 x) {
@@ -600,7 +631,7 @@ attn_split_kernel(const AttnArgs a) {
         run.n = blockIdx.x / per;
         run.u = 0;
         run.end = 1;
-    } else run = find_run<kAttnThreads>(c, a.window, per, kMinUnits, a.status);
+    } else run = find_run<kAttnThreads>(c, a.window, per, kMinUnits, a.status, blockIdx.x, gridDim.x);
 
     R ring{a, tc::smem_addr(smem) + warp * R::kBytes, warp, lane, run};
     ring.open();
@@ -622,7 +653,7 @@ attn_split_kernel(const AttnArgs a) {
             cp_async_wait<kStages - 1>();
             __syncwarp();
             const int tok = (i * kAttnWarps + warp) * En::KW;  // in the segment
-            float *sc = a.scores ? a.scores + ((sg.unit + tok / kUnit) * a.hpb) * kUnit + tok % kUnit : nullptr;
+            float *sc = a.scores ? a.scores + (size_t)(sg.unit + tok / kUnit) * a.hpb * kUnit + tok % kUnit : nullptr;
             const uint32_t st = ring.base + stage * R::kStage;
             if (live) en.template step<R>(a, sg, st, st + R::kHalf, live, lane, sc, own);
             stage = stage == kStages - 1 ? 0 : stage + 1;
@@ -658,21 +689,21 @@ attn_split_kernel(const AttnArgs a) {
         if constexpr (!SOLO) {
             if (tid == 0 && sg.starts)
                 a.parts[(size_t)sg.n * per + sg.run] =
-                    sg.whole ? make_int2(-1, -1) : make_int2((int)blockIdx.x, (int)((sg.run_end - 1) / run.share));
+                    sg.whole ? make_int2(-1, -1) : make_int2((int)blockIdx.x, (sg.run_end - 1) / run.share);
         }
         __syncthreads();  // the area is a stage again
     }
     cp_async_wait<0>();
 }
 
-// One block a (sequence, query head): joins its parts, or writes the empty
-// sequence's result, or (no parts: it is written already) ends.  Each of the
-// block's groups of D / 4 lanes takes every kGroups-th part, four loads ahead.
-// One sequence alone leaves a part in every block of the GPU, and then the
-// blocks here are few and have 1024 threads (NT); otherwise 128.
+// After the split.  The first N H blocks: one a (sequence, query head) that
+// joins its parts, or writes the empty sequence's result, or (no parts: it is
+// written already) ends.  Each of a block's groups of D / 4 lanes takes every
+// kGroups-th part, four loads ahead.  One sequence alone leaves a part in
+// every block of the GPU, and then the blocks here are few and have 1024
+// threads (NT); otherwise 128.
 template <typename E, int D, int NT>
-__global__ void __launch_bounds__(NT)
-attn_join_kernel(const AttnArgs a) {
+__device__ __forceinline__ void join_head(const AttnArgs &a) {
     constexpr int kLanes = D / 4, kGroups = NT / kLanes, kAhead = 4;
     __shared__ float s_m[NT / 32];
     __shared__ float s_l[kGroups];
@@ -681,29 +712,21 @@ attn_join_kernel(const AttnArgs a) {
     const int hb = g / a.hpb, row = g - hb * a.hpb;
     const size_t hd = blockIdx.x;
     E *o = static_cast<E *>(a.o) + hd * D;
-    allow_next_launch();
-    wait_for_previous();
     if (checked_len(a.c, n, a.status) == 0) {
-        if (tid < kLanes) store4(o + tid * 4, make_float4(0.f, 0.f, 0.f, 0.f));
-        if (tid == 0) {
-            if (a.lse) a.lse[hd] = -INFINITY;
-            if (a.lse2) a.lse2[hd] = -INFINITY;
-        }
+        if (tid < kLanes) write_result(a, o + tid * 4, hd, tid == 0, -INFINITY, 0.f, make_float4(0.f, 0.f, 0.f, 0.f));
         return;
     }
     const int2 pr = a.parts[((size_t)n * a.c.Hkv + kvh) * a.HB + hb];
     if (pr.x < 0) return;
-    // block pr.x has the run's beginning (its second part), the others their first
-    auto slot = [&](int b) { return (size_t)(2 * b + (b == pr.x)) * kHeadBlock + row; };
     const int grp = tid / kLanes, ch = tid - grp * kLanes;
     float4 v[kAhead];
 #pragma unroll
     for (int i = 0; i < kAhead; ++i) {  // the first parts come while the maximum is found
         const int b = pr.x + grp + i * kGroups;
-        if (b <= pr.y) v[i] = *reinterpret_cast<const float4 *>(a.part + slot(b) * D + ch * 4);
+        if (b <= pr.y) v[i] = *reinterpret_cast<const float4 *>(a.part + part_row(pr, b, row) * D + ch * 4);
     }
     float m = -INFINITY;
-    for (int b = pr.x + tid; b <= pr.y; b += NT) m = fmaxf(m, a.ml[slot(b)].x);
+    for (int b = pr.x + tid; b <= pr.y; b += NT) m = fmaxf(m, a.ml[part_row(pr, b, row)].x);
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
     if ((tid & 31) == 0) s_m[tid >> 5] = m;
@@ -717,8 +740,8 @@ attn_join_kernel(const AttnArgs a) {
 #pragma unroll
         for (int i = 0; i < kAhead; ++i) {
             const int b = b0 + i * kGroups;
-            y[i] = b <= pr.y ? a.ml[slot(b)] : make_float2(-INFINITY, 0.f);
-            if (b0 != pr.x + grp && b <= pr.y) v[i] = *reinterpret_cast<const float4 *>(a.part + slot(b) * D + ch * 4);
+            y[i] = b <= pr.y ? a.ml[part_row(pr, b, row)] : make_float2(-INFINITY, 0.f);
+            if (b0 != pr.x + grp && b <= pr.y) v[i] = *reinterpret_cast<const float4 *>(a.part + part_row(pr, b, row) * D + ch * 4);
         }
 #pragma unroll
         for (int i = 0; i < kAhead; ++i) {
@@ -743,17 +766,18 @@ attn_join_kernel(const AttnArgs a) {
     write_result(a, o + tid * 4, hd, tid == 0, m, l, x);
 }
 
-// weight_j += sum over the group's heads of 2^(s_j - lse), from the scores the
-// split kernel kept: 64 threads a unit, a token each.  One addition a token and
-// call, so the sums do not depend on any order unless sequences share a page.
-constexpr int kWeightThreads = 256;
-__global__ void __launch_bounds__(kWeightThreads)
-attn_weights_kernel(const AttnArgs a, int solo) {
+// The blocks behind those (first = N H; none unless weights are wanted):
+//   weight_j += sum over the group's heads of 2^(s_j - lse),
+// from the scores that the split kernel kept, 64 threads a unit, a token each.
+// A head's lse is the one written, or comes from its parts once more.  One
+// addition a token and call, so that no order matters unless sequences share
+// the page.
+template <int NT, bool SOLO>
+__device__ __forceinline__ void add_weights(const AttnArgs &a, int first_block) {
+    __shared__ float s_L[kMostGroup];
     const PagedView &c = a.c;
-    allow_next_launch();
-    wait_for_previous();
-    Run run = find_run<kWeightThreads>(c, a.window, c.Hkv, 1, a.status);
-    const int half = threadIdx.x / kUnit, tok = threadIdx.x % kUnit;
+    Run run = find_run<NT>(c, a.window, c.Hkv, 1, a.status, blockIdx.x - first_block, gridDim.x - first_block);
+    const int tid = threadIdx.x, lane = tid & 31, sub = tid / kUnit, tok = tid % kUnit;
     while (run.u < run.end) {
         const int len = checked_len(c, run.n, a.status), first = first_token(len, a.window);
         const int T = (len - first + kUnit - 1) / kUnit;
@@ -761,10 +785,31 @@ attn_weights_kernel(const AttnArgs a, int solo) {
             ++run.n;
             continue;
         }
-        const int h = (int)((run.u - run.base) / T), t0 = (int)((run.u - run.base) - (long long)h * T);
-        const int cnt = (int)(T - t0 < run.end - run.u ? T - t0 : run.end - run.u);
-        const float *L = a.lse2 + (size_t)run.n * a.H + h * a.G;
-        for (int t = t0 + half; t < t0 + cnt; t += kWeightThreads / kUnit) {
+        const int h = (run.u - run.base) / T, t0 = run.u - run.base - h * T;
+        const int cnt = min(T - t0, run.end - run.u);
+        __syncthreads();  // the last segment's s_L has been read
+        for (int g = tid >> 5; g < a.G; g += NT / 32) {
+            const int hb = g / a.hpb, row = g - hb * a.hpb;
+            const int2 pr = SOLO ? make_int2(-1, -1) : a.parts[((size_t)run.n * c.Hkv + h) * a.HB + hb];
+            float L;
+            if (pr.x < 0) L = a.lse2[(size_t)run.n * a.H + h * a.G + g];
+            else {
+                float m = -INFINITY, l = 0.f;
+                for (int b = pr.x + lane; b <= pr.y; b += 32) m = fmaxf(m, a.ml[part_row(pr, b, row)].x);
+#pragma unroll
+                for (int off = 16; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
+                for (int b = pr.x + lane; b <= pr.y; b += 32) {
+                    const float2 y = a.ml[part_row(pr, b, row)];
+                    l += part_factor(y, m) * y.y;
+                }
+#pragma unroll
+                for (int off = 16; off > 0; off >>= 1) l += __shfl_xor_sync(0xffffffffu, l, off);
+                L = l == 0.f ? -INFINITY : m + log2f(l);
+            }
+            if (lane == 0) s_L[g] = L;
+        }
+        __syncthreads();
+        for (int t = t0 + sub; t < t0 + cnt; t += NT / kUnit) {
             const int j = first + t * kUnit + tok;
             if (j >= len) continue;
             int entry, slot;
@@ -774,24 +819,35 @@ attn_weights_kernel(const AttnArgs a, int solo) {
             float sum = 0.f;
             for (int hb = 0; hb < a.HB; ++hb) {
                 // the split kernel's number of this unit: it has Hkv HB runs a sequence
-                const long long run_of = (long long)h * a.HB + hb;
-                const long long unit = solo ? ((long long)run.n * c.Hkv * a.HB + run_of) * ((c.cap + kUnit - 1) / kUnit) + t
-                                            : run.base * a.HB + run_of * T + t;
-                const float *s = a.scores + unit * a.hpb * kUnit + tok;
+                const int run_of = h * a.HB + hb;
+                const int unit = SOLO ? (run.n * c.Hkv * a.HB + run_of) * ((c.cap + kUnit - 1) / kUnit) + t
+                                      : run.base * a.HB + run_of * T + t;
+                const float *s = a.scores + (size_t)unit * a.hpb * kUnit + tok;
                 const int rows = min(a.hpb, a.G - hb * a.hpb);
+#pragma unroll 4
                 for (int r = 0; r < rows; ++r) {
-                    const float Lr = L[hb * a.hpb + r];
-                    sum += Lr == -INFINITY ? 0.f : exp2f(s[r * kUnit] - Lr);
+                    const float L = s_L[hb * a.hpb + r];
+                    sum += L == -INFINITY ? 0.f : exp2f(s[r * kUnit] - L);
                 }
             }
             atomicAdd(c.w + weight_off(c, page, slot, h), sum);
         }
         run.u += cnt;
-        if (run.u == run.base + (long long)c.Hkv * T) {
+        if (run.u == run.base + c.Hkv * T) {
             run.base = run.u;
             ++run.n;
         }
     }
+}
+
+template <typename E, int D, int NT, bool SOLO>
+__global__ void __launch_bounds__(NT)
+attn_finish_kernel(const AttnArgs a) {
+    allow_next_launch();
+    wait_for_previous();
+    const int heads = SOLO ? 0 : a.c.N * a.H;
+    if (!SOLO && blockIdx.x < heads) join_head<E, D, NT>(a);
+    else add_weights<NT, SOLO>(a, heads);
 }
 
 // ---- host side
@@ -804,18 +860,28 @@ static void head_blocks(const PagedView &c, int H, AttnArgs &a) {
 
 // places the workspace's regions (ws may be null: sizes only); returns its bytes
 static size_t attn_ws(const PagedView &c, AttnArgs &a, int add_weights, void *ws) {
+    a.ml = nullptr;
+    a.part = a.lse2 = a.scores = nullptr;
+    a.parts = nullptr;
+    if (c.cap <= kSoloTokens && !add_weights) return 256;  // not touched
     const size_t slots = 2 * (size_t)kMostBlocksPerSm * sm_count(), runs = (size_t)c.N * c.Hkv * a.HB;
     size_t o = 0;
     auto take = [&](size_t bytes) { const size_t at = o; o = align256(o + bytes); return static_cast<char *>(ws) + at; };
     a.ml = reinterpret_cast<float2 *>(take(slots * kHeadBlock * sizeof(float2)));
     a.part = reinterpret_cast<float *>(take(slots * kHeadBlock * c.d * sizeof(float)));
     a.parts = reinterpret_cast<int2 *>(take(runs * sizeof(int2)));
-    a.lse2 = a.scores = nullptr;
     if (add_weights) {
         a.lse2 = reinterpret_cast<float *>(take((size_t)c.N * a.H * sizeof(float)));
         a.scores = reinterpret_cast<float *>(take(runs * ((c.cap + kUnit - 1) / kUnit) * a.hpb * kUnit * sizeof(float)));
     }
     return o;
+}
+
+// units of 64 tokens that the call may have to count
+bool attn_countable(const PagedView &c, int H) {
+    AttnArgs a;
+    head_blocks(c, H, a);
+    return (double)c.N * c.Hkv * a.HB * ((c.cap + kUnit - 1) / kUnit) < (double)(1 << 30);
 }
 
 size_t attn_ws_bytes(const PagedView &c, int H, int add_weights) {
@@ -835,13 +901,12 @@ static cudaError_t attn_run_as(const AttnArgs &a, cudaStream_t s) {
     e = launch_behind(K_ATTN_SPLIT, attn_split_kernel<En, D, SOLO>,
                       SOLO ? a.c.N * a.c.Hkv * a.HB : En::kBlocksPerSm * sm_count(), kAttnThreads, bytes, s, a);
     if (e != cudaSuccess) return e;
-    if (!SOLO) {
-        e = heads <= sm_count() ? launch_behind(K_ATTN_JOIN, attn_join_kernel<E, D, 1024>, heads, 1024, 0, s, a)
-                                : launch_behind(K_ATTN_JOIN, attn_join_kernel<E, D, 128>, heads, 128, 0, s, a);
-        if (e != cudaSuccess) return e;
-    }
-    if (!a.scores) return cudaSuccess;
-    return launch_behind(K_ATTN_WEIGHTS, attn_weights_kernel, 8 * sm_count(), kWeightThreads, 0, s, a, (int)SOLO);
+    if (SOLO && !a.scores) return cudaSuccess;
+    if (heads <= sm_count())
+        return launch_behind(K_ATTN_FINISH, attn_finish_kernel<E, D, 1024, SOLO>, (SOLO ? 0 : heads) + (a.scores ? 2 * sm_count() : 0),
+                             1024, 0, s, a);
+    return launch_behind(K_ATTN_FINISH, attn_finish_kernel<E, D, 128, SOLO>, (SOLO ? 0 : heads) + (a.scores ? 12 * sm_count() : 0),
+                         128, 0, s, a);
 }
 template <class En, int D>
 static cudaError_t attn_run(const AttnArgs &a, cudaStream_t s) {

@@ -7,9 +7,9 @@
 // whose unsigned order is the floats' order: three digits of 11, 11 and 10
 // bits, each a histogram of the digit among the keys that share the prefix
 // found so far and a scan of it from the top.  It then lists the kept tokens
-// in their order.  A cluster of up to 8 blocks shares one (sequence, head);
-// each holds its slice of the keys in shared memory, so the weights are read
-// once, and sums the others' histograms over distributed shared memory.
+// in their order.  A cluster of up to 16 blocks shares one (sequence,
+// head); each holds its slice of the keys in shared memory, so the weights are
+// read once, and sums the others' histograms over distributed shared memory.
 //
 // Carrying the rows is a copy bound by HBM: evict_copy for another cache, and
 // evict_shift in place, where a row may overwrite one that is still to be read.
@@ -22,10 +22,9 @@ namespace cg = cooperative_groups;
 
 namespace gdn2 {
 
-constexpr int kSelThreads = 512;
-constexpr int kSelWarps = kSelThreads / 32;
 constexpr int kBins = 2048;
 constexpr int kDigits = 3;
+constexpr int kMostRanks = 16;     // blocks of a cluster
 constexpr int kMaxKeys = 40960;    // keys of a block's slice in shared memory
 constexpr int kMoveThreads = 256;
 
@@ -51,7 +50,8 @@ __device__ __forceinline__ unsigned key_at(const PagedView &c, int n, int h, int
     return weight_key(c.w[weight_off(c, page, slot, h)]);
 }
 
-// inclusive scan over the block's threads
+// inclusive scan over the block's NT threads
+template <int NT>
 __device__ __forceinline__ int block_scan(int x, int *warp_tot) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
 #pragma unroll
@@ -61,9 +61,9 @@ __device__ __forceinline__ int block_scan(int x, int *warp_tot) {
     }
     if (lane == 31) warp_tot[warp] = x;
     __syncthreads();
-    int t = lane < kSelWarps ? warp_tot[lane] : 0;
+    int t = lane < NT / 32 ? warp_tot[lane] : 0;
 #pragma unroll
-    for (int off = 1; off < kSelWarps; off <<= 1) {
+    for (int off = 1; off < NT / 32; off <<= 1) {
         const int y = __shfl_up_sync(0xffffffffu, t, off);
         if (lane >= off) t += y;
     }
@@ -74,13 +74,15 @@ __device__ __forceinline__ int block_scan(int x, int *warp_tot) {
 
 // Block (n h, rank) of a cluster.  slots: the keys that dynamic shared memory
 // holds; stride: entries of a list.
-__global__ void __launch_bounds__(kSelThreads)
+template <int NT>
+__global__ void __launch_bounds__(NT)
 evict_select_kernel(const PagedView c, const PagedView to, int in_place, int budget, int sink, int recent,
                     int slots, int stride, int *list_all, EvictPlan *plan, unsigned int *status) {
+    constexpr int kWarps = NT / 32, kOwn = kBins / NT;  // digits of a thread
     extern __shared__ unsigned s_key[];
     __shared__ __align__(16) int hist[kDigits][kBins];
     __shared__ int warp_tot[32], s_digit, s_above;
-    __shared__ int2 s_warp[kSelWarps];  // kept for certain, equal to the threshold: a warp's
+    __shared__ int2 s_warp[kWarps];  // kept for certain, equal to the threshold: a warp's
     __shared__ int2 s_block;            // the block's
     __shared__ int s_first;
     cg::cluster_group cluster = cg::this_cluster();
@@ -97,13 +99,13 @@ evict_select_kernel(const PagedView c, const PagedView to, int in_place, int bud
         len = 0;
     }
     if (len <= budget) {
-        for (int j = rank * kSelThreads + tid; j < stride; j += ranks * kSelThreads) list[j] = j < len ? j : -1;
+        for (int j = rank * NT + tid; j < stride; j += ranks * NT) list[j] = j < len ? j : -1;
         if (rank == 0 && tid == 0) plan[nh] = EvictPlan{in_place ? len : 0, in_place && raw != len ? -1 : len};
         return;
     }
     const int lo = sink, hi = len - recent, T = budget - sink - recent;  // T < hi - lo
-    for (int j = rank * kSelThreads + tid; j < sink; j += ranks * kSelThreads) list[j] = j;
-    for (int j = rank * kSelThreads + tid; j < recent; j += ranks * kSelThreads) list[budget - recent + j] = hi + j;
+    for (int j = rank * NT + tid; j < sink; j += ranks * NT) list[j] = j;
+    for (int j = rank * NT + tid; j < recent; j += ranks * NT) list[budget - recent + j] = hi + j;
     if (T == 0) {
         if (rank == 0 && tid == 0) plan[nh] = EvictPlan{in_place ? sink : 0, budget};
         return;
@@ -111,16 +113,16 @@ evict_select_kernel(const PagedView c, const PagedView to, int in_place, int bud
     const int per = (hi - lo + ranks - 1) / ranks, a = min(hi, lo + rank * per), b = min(hi, a + per);
     const bool held = per <= slots;
     auto key = [&](int j) { return held ? s_key[j - a] : key_at(c, n, h, j, status); };
-    for (int x = tid; x < kDigits * kBins; x += kSelThreads) (&hist[0][0])[x] = 0;
+    for (int x = tid; x < kDigits * kBins; x += NT) (&hist[0][0])[x] = 0;
     if (tid == 0) s_first = len;
     if (held) {  // eight at a time, each load before any is used
         constexpr int kAhead = 8;
-        for (int j0 = a + tid; j0 < b; j0 += kAhead * kSelThreads) {
+        for (int j0 = a + tid; j0 < b; j0 += kAhead * NT) {
             int page[kAhead], slot[kAhead];
             float w[kAhead];
 #pragma unroll
             for (int u = 0; u < kAhead; ++u) {
-                const int j = min(j0 + u * kSelThreads, b - 1);
+                const int j = min(j0 + u * NT, b - 1);
                 int entry;
                 page_slot(c, j, entry, slot[u]);
                 page[u] = page_of(c, n, entry);
@@ -130,7 +132,7 @@ evict_select_kernel(const PagedView c, const PagedView to, int in_place, int bud
 #pragma unroll
             for (int u = 0; u < kAhead; ++u) {
                 if (page[u] < 0) record_status(status, GDN2_ERR_INVALID_ARG);
-                if (j0 + u * kSelThreads < b) s_key[j0 + u * kSelThreads - a] = weight_key(w[u]);
+                if (j0 + u * NT < b) s_key[j0 + u * NT - a] = weight_key(w[u]);
             }
         }
     }
@@ -140,27 +142,45 @@ evict_select_kernel(const PagedView c, const PagedView to, int in_place, int bud
 #pragma unroll
     for (int d = 0; d < kDigits; ++d) {
         const int shift = d == 0 ? 21 : d == 1 ? 10 : 0, width = d == 2 ? 10 : 11;
-        for (int j = a + tid; j < b; j += kSelThreads) {
+        for (int j = a + tid; j < b; j += NT) {
             const unsigned k = key(j);
             if ((k & mask) == prefix) atomicAdd(&hist[d][(k >> shift) & ((1u << width) - 1)], 1);
         }
         cluster.sync();
-        // thread t: the t-th four digits from the top
-        static_assert(kBins == 4 * kSelThreads, "four bins a thread");
-        const int top = kBins - 1 - 4 * tid;
-        int4 x = make_int4(0, 0, 0, 0);
-        for (int r = 0; r < ranks; ++r) {
-            const int4 y = *reinterpret_cast<const int4 *>(cluster.map_shared_rank(&hist[d][top - 3], r));
-            x.x += y.x; x.y += y.y; x.z += y.z; x.w += y.w;
+        // Each block sums its share of the bins over the cluster, in place (the
+        // others read only their own shares of it), and then reads the sums:
+        // two short trips over the cluster's network instead of every block
+        // reading all of every histogram.
+        const int share = kBins / ranks;
+        if (ranks > 1) {
+            for (int i = tid; i < share; i += NT) {
+                int sum = 0;
+#pragma unroll
+                for (int r = 0; r < kMostRanks; ++r)
+                    if (r < ranks) sum += *cluster.map_shared_rank(&hist[d][rank * share + i], r);
+                hist[d][rank * share + i] = sum;
+            }
+            cluster.sync();
         }
-        const int inc = block_scan(x.x + x.y + x.z + x.w, warp_tot);
-        int above = inc - x.x - x.y - x.z - x.w;
-        if (above < need && need <= inc) {  // one thread
-            int digit = top;
-            if (above + x.w < need) { above += x.w; --digit;
-                if (above + x.z < need) { above += x.z; --digit;
-                    if (above + x.y < need) { above += x.y; --digit; } } }
-            s_digit = digit;
+        // thread t: the t-th kOwn digits from the top
+        const int top = kBins - 1 - kOwn * tid;
+        int own[kOwn];
+        const int *summed = cluster.map_shared_rank(&hist[d][top - kOwn + 1], (top - kOwn + 1) / share);
+#pragma unroll
+        for (int i = 0; i < kOwn; i += 2) {
+            const int2 y = *reinterpret_cast<const int2 *>(summed + i);
+            own[i] = y.x;
+            own[i + 1] = y.y;
+        }
+        int sum = 0;
+#pragma unroll
+        for (int i = 0; i < kOwn; ++i) sum += own[i];
+        const int inc = block_scan<NT>(sum, warp_tot);
+        int above = inc - sum;
+        if (above < need && need <= inc) {  // one thread: its digit with the need-th largest
+            int i = kOwn - 1;
+            for (; i > 0 && above + own[i] < need; --i) above += own[i];
+            s_digit = top - kOwn + 1 + i;
             s_above = above;
         }
         __syncthreads();
@@ -171,7 +191,7 @@ evict_select_kernel(const PagedView c, const PagedView to, int in_place, int bud
     }
     // all keys above `prefix` stay, and the first `need` of those equal to it.
     // Each warp takes a contiguous piece of the slice: first it counts.
-    const int piece = ((b - a + kSelWarps - 1) / kSelWarps + 31) / 32 * 32;
+    const int piece = ((b - a + kWarps - 1) / kWarps + 31) / 32 * 32;
     const int wa = min(b, a + warp * piece), wb = min(b, wa + piece);
     int2 cnt = make_int2(0, 0);
     for (int j0 = wa; j0 < wb; j0 += 32) {
@@ -183,7 +203,7 @@ evict_select_kernel(const PagedView c, const PagedView to, int in_place, int bud
     if (lane == 0) s_warp[warp] = cnt;
     __syncthreads();
     int2 before = make_int2(0, 0);
-    for (int w = 0; w < kSelWarps; ++w) {
+    for (int w = 0; w < kWarps; ++w) {
         const int2 x = s_warp[w];
         if (w == warp) cnt = before;
         before.x += x.x;
@@ -191,11 +211,14 @@ evict_select_kernel(const PagedView c, const PagedView to, int in_place, int bud
     }
     if (tid == 0) s_block = before;
     cluster.sync();
-    for (int r = 0; r < rank; ++r) {
-        const int2 x = *cluster.map_shared_rank(&s_block, r);
-        cnt.x += x.x;
-        cnt.y += x.y;
+    int2 other = lane < rank ? *cluster.map_shared_rank(&s_block, lane) : make_int2(0, 0);
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) {
+        other.x += __shfl_xor_sync(0xffffffffu, other.x, off);
+        other.y += __shfl_xor_sync(0xffffffffu, other.y, off);
     }
+    cnt.x += other.x;
+    cnt.y += other.y;
     int first = len;  // the first token that goes: up to there no row moves
     const unsigned below = (1u << lane) - 1;
     for (int j0 = wa; j0 < wb; j0 += 32) {
@@ -213,9 +236,11 @@ evict_select_kernel(const PagedView c, const PagedView to, int in_place, int bud
     }
     if (first < len) atomicMin(&s_first, first);
     cluster.sync();
-    if (rank == 0 && tid == 0) {
-        for (int r = 0; r < ranks; ++r) first = min(first, *cluster.map_shared_rank(&s_first, r));
-        plan[nh] = EvictPlan{in_place ? first : 0, budget};
+    if (rank == 0 && warp == 0) {
+        first = lane < ranks ? *cluster.map_shared_rank(&s_first, lane) : len;
+#pragma unroll
+        for (int off = 16; off > 0; off >>= 1) first = min(first, __shfl_xor_sync(0xffffffffu, first, off));
+        if (lane == 0) plan[nh] = EvictPlan{in_place ? first : 0, budget};
     }
     cluster.sync();  // no block ends while another reads its memory
 }
@@ -389,6 +414,18 @@ static cudaError_t shift_launch(const PagedView &c, int stride, const int *list,
                          kMoveThreads, 0, s, c, stride, list, plan, status);
 }
 
+template <int NT>
+static cudaError_t select_launch(const PagedView &src, const PagedView &dst, bool in_place, int budget, int sink, int recent,
+                                 int ranks, int slots, int stride, int *list, EvictPlan *plan, unsigned int *status,
+                                 cudaStream_t s) {
+    const auto kernel = evict_select_kernel<NT>;
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxKeys * 4);
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (e != cudaSuccess) return e;
+    return launch_clusters(K_EVICT_SELECT, kernel, ranks, src.N * src.Hkv * ranks, NT, slots * 4, s, src, dst, (int)in_place,
+                           budget, sink, recent, slots, stride, list, plan, status);
+}
+
 cudaError_t evict_launch(const PagedView &src, const PagedView &dst, bool in_place, int budget, int sink,
                          int recent, int *kept, void *ws, unsigned int *status, cudaStream_t s) {
     const int nh = src.N * src.Hkv;
@@ -397,12 +434,12 @@ cudaError_t evict_launch(const PagedView &src, const PagedView &dst, bool in_pla
     int *list = kept ? kept : at<int>(ws, align256((size_t)nh * sizeof(EvictPlan)));
     // blocks of a cluster: until a slice is 4096 tokens or the GPU is full
     int ranks = 1;
-    while (ranks < 8 && src.cap / ranks > 4096 && (long long)nh * ranks < sm_count()) ranks *= 2;
-    const int slots = (int)(((long long)src.cap + ranks - 1) / ranks < kMaxKeys ? (src.cap + ranks - 1) / ranks : kMaxKeys);
-    cudaError_t e = cudaFuncSetAttribute(evict_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxKeys * 4);
-    if (e != cudaSuccess) return e;
-    e = launch_clusters(K_EVICT_SELECT, evict_select_kernel, ranks, nh * ranks, kSelThreads, slots * 4, s, src, dst,
-                        (int)in_place, budget, sink, recent, slots, stride, list, plan, status);
+    while (ranks < kMostRanks && src.cap / ranks > 4096 && (long long)nh * ranks < sm_count()) ranks *= 2;
+    const int slice = (int)(((long long)src.cap + ranks - 1) / ranks), slots = slice < kMaxKeys ? slice : kMaxKeys;
+    // one block an SM has 1024 threads; several hide each other's waits with 512
+    cudaError_t e = (long long)nh * ranks <= sm_count()
+                        ? select_launch<1024>(src, dst, in_place, budget, sink, recent, ranks, slots, stride, list, plan, status, s)
+                        : select_launch<512>(src, dst, in_place, budget, sink, recent, ranks, slots, stride, list, plan, status, s);
     if (e != cudaSuccess) return e;
     if (in_place) {
         const long long narrow = (long long)nh * 2 * (src.d * src.es / 16);  // blocks of 16-byte columns

@@ -6,6 +6,8 @@
 
 namespace gdn2 {
 
+constexpr int kMaxHeadGroup = 256;  // most query heads of a key-value head
+
 struct PagedView {
     char *k, *v;
     float *w;          // [num_pages, Hkv, page] or nullptr
@@ -82,6 +84,7 @@ static cudaError_t launch_behind(int kind, void (*kernel)(P...), int grid, int t
 
 cudaError_t kv_append_launch(const PagedView &c, const void *k, const void *v, const int *cu, int T,
                              int *lens_out, unsigned int *status, cudaStream_t s);
+bool attn_countable(const PagedView &c, int H);
 size_t attn_ws_bytes(const PagedView &c, int H, int add_weights);
 cudaError_t attn_launch(const PagedView &c, const void *q, void *o, float *lse, int H, float scale,
                         int window, int add_weights, void *ws, unsigned int *status, cudaStream_t s);

@@ -286,13 +286,15 @@ gdn2_status gdn2_kv_append(const gdn2_paged_kv *kv, const void *k, const void *v
                            const int *cu_seqlens, int T, int *lens_out, gdn2_stream_t stream);
 
 /* Bytes of device workspace (at least 256) that gdn2_attn_decode_step needs for
- * H query heads on the current device; 0 where the sizes are unsupported. */
+ * H query heads on the current device; 0 where the sizes are unsupported.  256
+ * says that the call does not touch it, so that calls at once may share it. */
 size_t gdn2_attn_decode_workspace_bytes(const gdn2_paged_kv *kv, int H, int add_weights);
 
 /* Softmax attention of one new token a sequence over its cached tokens:
  *   s_j = scale <q, k_j>, j in [max(0, len - window), len) (window = 0: all),
  *   o = sum_j e^(s_j - lse) v_j,   lse = log sum_j e^(s_j).
- * Query head h reads key-value head h / (H / H_kv); H a multiple of H_kv.  The
+ * Query head h reads key-value head h / (H / H_kv); H a multiple of H_kv, at
+ * most 256 times it, and N * H * max_pages * page_size < 2^36.  The
  * new token attends to itself once it has been appended.
  *   q, o : [N, H, d] contiguous, io type.   lse : float32 [N, H], or NULL.
  *   A sequence without tokens gets o = 0 and lse = -inf.
