@@ -35,7 +35,6 @@ constexpr int kUnit = 64;        // tokens of a unit
 constexpr int kMostBlocksPerSm = 4;
 constexpr int kMostGroup = kMaxHeadGroup;
 constexpr int kHeadBlock = 16;   // most query heads of one pass
-constexpr int kStages = 3;
 constexpr int kMinUnits = 2;     // fewest units worth a block of their own
 // Tables that reach no further than this give each block one (sequence, head)
 // whole: no search for a run, no join.
@@ -132,6 +131,9 @@ __device__ __forceinline__ Run find_run(const PagedView &c, int window, int per,
 __device__ __forceinline__ void cp_async16_zfill(uint32_t dst, const void *src, bool valid) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(valid ? 16 : 0) : "memory");
 }
+__device__ __forceinline__ void cp_async16_full(uint32_t dst, const void *src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
 template <int N> __device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
 
 __device__ __forceinline__ void ldmatrix4(uint32_t addr, uint32_t *r) {
@@ -217,12 +219,14 @@ __device__ __forceinline__ bool next_segment(const AttnArgs &a, Run &run, Segmen
 // of row r at p ^ key(r)), so that eight rows' equal pieces lie in different
 // banks.  Rows without a token are zeros: their v must not be whatever the
 // memory held, since 0 times NaN is NaN.
-template <int KW, int RB, bool SOLO>
+template <int KW, int RB, int STAGES, bool SOLO>
 struct Ring {
+    static constexpr int kStages = STAGES;
     static constexpr int kPieces = RB / 16;
     static constexpr int kHalf = KW * RB, kStage = 2 * kHalf;
     static constexpr int kBytes = kStages * kStage;
     static constexpr int kStep = kAttnWarps * KW;
+    static constexpr uint32_t kAllRows = (1u << KW) - 1;
     const AttnArgs &a;
     uint32_t base;  // this warp's stages
     int warp, lane;
@@ -269,6 +273,27 @@ struct Ring {
         at_tok += kStep;
         if (--steps == 0) open();
     }
+    // the copies of a step to stage s, from lane r % KW's row r at `off`;
+    // FULL: every row holds a token, otherwise those that do not become zeros
+    template <bool FULL> __device__ __forceinline__ void copy(uint32_t s, long long off) const {
+        constexpr int kRowsAtOnce = 32 / kPieces;  // rows of one instruction
+        static_assert(kPieces <= 32 && KW * kPieces % 32 == 0, "whole warps of pieces");
+        const int piece = lane % kPieces, mine = lane / kPieces;
+        const char *k = a.c.k + piece * 16, *v = a.c.v + piece * 16;
+#pragma unroll
+        for (int x = 0; x < KW * kPieces / 32; ++x) {
+            const int r = x * kRowsAtOnce + mine;
+            const long long ro = __shfl_sync(0xffffffffu, off, r);
+            const uint32_t to = s + at(r, piece);
+            if (FULL) {
+                cp_async16_full(to, k + ro);
+                cp_async16_full(to + kHalf, v + ro);
+            } else {
+                cp_async16_zfill(to, ro < 0 ? k : k + ro, ro >= 0);
+                cp_async16_zfill(to + kHalf, ro < 0 ? v : v + ro, ro >= 0);
+            }
+        }
+    }
     // starts the copies of the step that was looked up (a group of its own,
     // empty past the last), and looks the one behind it up
     __device__ __forceinline__ uint32_t issue(int stage) {
@@ -280,16 +305,8 @@ struct Ring {
         const uint32_t ok = __ballot_sync(0xffffffffu, off >= 0);
         if (ready) {
             const uint32_t s = base + stage * kStage;
-            constexpr int kRowsAtOnce = 32 / kPieces;  // rows of one instruction
-            static_assert(kPieces <= 32 && KW * kPieces % 32 == 0, "whole warps of pieces");
-#pragma unroll
-            for (int x = 0; x < KW * kPieces / 32; ++x) {
-                const int r = x * kRowsAtOnce + lane / kPieces, piece = lane % kPieces;
-                const long long ro = __shfl_sync(0xffffffffu, off, r);
-                const long long from = (ro < 0 ? 0 : ro) + piece * 16;
-                cp_async16_zfill(s + at(r, piece), a.c.k + from, ro >= 0);
-                cp_async16_zfill(s + kHalf + at(r, piece), a.c.v + from, ro >= 0);
-            }
+            if ((ok & kAllRows) == kAllRows) copy<true>(s, off);
+            else copy<false>(s, off);
         }
         tc::cp_async_commit();
         lookup();
@@ -310,7 +327,7 @@ template <int D> __device__ __forceinline__ int merge_at(int row, int ch) { retu
 template <int D, int NT>
 struct EngineBf16 {
     using E = __nv_bfloat16;
-    static constexpr int KW = 16, RB = 2 * D, kRows = 8 * NT, kBlocksPerSm = D == 128 ? 2 : 4;
+    static constexpr int KW = 16, RB = 2 * D, kRows = 8 * NT, kBlocksPerSm = D == 128 ? 2 : 4, kStages = 3;
     uint32_t qf[NT][D / 16][2];
     float acc[NT][D / 16][4];
     float m[NT][2], l[NT][2];
@@ -440,14 +457,16 @@ struct EngineBf16 {
 template <int D, int GP>
 struct EngineF32 {
     using E = float;
-    static constexpr int KT = 1;
-    static constexpr int KW = 8 * KT, RB = 4 * D, kRows = GP;
-    static constexpr int kBlocksPerSm = D == 128 || GP == 16 ? 2 : GP == 8 ? 3 : 4;
+    static constexpr int KT = D == 128 || GP == 16 ? 1 : 2;
+    static constexpr int KW = 8 * KT, RB = 4 * D, kRows = GP, kStages = 3;
+    static constexpr int kBlocksPerSm = D == 32 && GP <= 4 ? 4 : 2;
     static constexpr int kLanes = D / 4;         // lanes of one token's channels
     static constexpr int kGroups = 32 / kLanes;  // tokens at once
-    static constexpr int kVec = GP < 4 ? GP : 4;
+    static constexpr int kVec = GP < 4 ? GP : 4;  // heads whose weights lie together, and that
+                                                  // the parts share out: part p's are p, p + 4, ..
+    static constexpr int kOwn = GP / kVec;
     float acc[GP][4];
-    float m[GP], l[GP];
+    float m[GP], l[kOwn * (GP < 4 ? GP : 1)];
 
     // sq: [GP][D] of the block's
     __device__ __forceinline__ void begin(const AttnArgs &a, const Segment &sg, int, float *sq) {
@@ -459,8 +478,14 @@ struct EngineF32 {
         for (int g = 0; g < GP; ++g) {
             acc[g][0] = acc[g][1] = acc[g][2] = acc[g][3] = 0.f;
             m[g] = -INFINITY;
-            l[g] = 0.f;
         }
+#pragma unroll
+        for (float &x : l) x = 0.f;
+    }
+    // of four heads' values the one of this lane's part
+    __device__ __forceinline__ static float of_part(const float *x, int part) {
+        const float lo = part & 1 ? x[1] : x[0], hi = part & 1 ? x[3] : x[2];
+        return part & 2 ? hi : lo;
     }
     // sp: [kAttnWarps][KW][GP] behind sq
     template <class R>
@@ -511,23 +536,39 @@ struct EngineF32 {
 #pragma unroll
                     for (int y = 0; y < KT; ++y) scores[g * kUnit + tok + 8 * y] = s[y][g];
         if (raised) {  // the same on every lane: m and mn are
+            float f[GP];
 #pragma unroll
             for (int g = 0; g < GP; ++g) {
-                const float f = mn[g] == m[g] ? 1.f : exp2f(m[g] - mn[g]);
+                f[g] = mn[g] == m[g] ? 1.f : exp2f(m[g] - mn[g]);
                 m[g] = mn[g];
-                l[g] *= f;
-                acc[g][0] *= f; acc[g][1] *= f; acc[g][2] *= f; acc[g][3] *= f;
+                acc[g][0] *= f[g]; acc[g][1] *= f[g]; acc[g][2] *= f[g]; acc[g][3] *= f[g];
+            }
+            if constexpr (GP >= 4) {
+#pragma unroll
+                for (int i = 0; i < kOwn; ++i) l[i] *= of_part(f + 4 * i, part);
+            } else {
+#pragma unroll
+                for (int g = 0; g < GP; ++g) l[g] *= f[g];
             }
         }
         __syncwarp();  // the last step's sp has been read
 #pragma unroll
-        for (int g = 0; g < GP; ++g) {
-            if (GP >= 4 && (g & 3) != part) continue;  // shared out among the four parts
+        for (int y = 0; y < KT; ++y) {
+            if constexpr (GP >= 4) {
 #pragma unroll
-            for (int y = 0; y < KT; ++y) {
-                const float e = exp2f(s[y][g] - (m[g] == -INFINITY ? 0.f : m[g]));
-                l[g] += e;
-                if (GP >= 4 || part == 0) sp[(tok + 8 * y) * GP + g] = e;
+                for (int i = 0; i < kOwn; ++i) {
+                    const float mp = of_part(m + 4 * i, part);
+                    const float e = exp2f(of_part(&s[y][4 * i], part) - (mp == -INFINITY ? 0.f : mp));
+                    l[i] += e;
+                    sp[(tok + 8 * y) * GP + 4 * i + part] = e;
+                }
+            } else {
+#pragma unroll
+                for (int g = 0; g < GP; ++g) {
+                    const float e = exp2f(s[y][g] - (m[g] == -INFINITY ? 0.f : m[g]));
+                    l[g] += e;
+                    if (part == 0) sp[(tok + 8 * y) * GP + g] = e;
+                }
             }
         }
         __syncwarp();
@@ -561,7 +602,7 @@ struct EngineF32 {
 #pragma unroll
         for (int g = 0; g < GP; ++g) {
             // a row's sum lies with one part's lanes (or, the same, with all four)
-            float x = GP >= 4 ? ((g & 3) == part ? l[g] : 0.f) : (part == 0 ? l[g] : 0.f);
+            float x = GP >= 4 ? ((g & 3) == part ? l[g / 4] : 0.f) : (part == 0 ? l[g % kVec] : 0.f);
 #pragma unroll
             for (int off = 1; off < 32; off <<= 1) x += __shfl_xor_sync(0xffffffffu, x, off);
             if (lane == 0) ml[g] = make_float2(m[g], x);
@@ -607,7 +648,7 @@ __device__ __forceinline__ void write_result(const AttnArgs &a, E *o, size_t hd,
 
 // shared memory of a block: the warps' rings, then what the engine keeps
 template <class En, int D> constexpr int attn_smem() {
-    return kAttnWarps * Ring<En::KW, En::RB, false>::kBytes +
+    return kAttnWarps * Ring<En::KW, En::RB, En::kStages, false>::kBytes +
            (sizeof(typename En::E) == 4 ? En::kRows * (D + kAttnWarps * En::KW) * 4 : 0);
 }
 
@@ -617,7 +658,8 @@ __global__ void __launch_bounds__(kAttnThreads, En::kBlocksPerSm)
 attn_split_kernel(const AttnArgs a) {
     extern __shared__ __align__(128) unsigned char smem[];
     __shared__ float2 s_ml[kAttnWarps][En::kRows];
-    using R = Ring<En::KW, En::RB, SOLO>;
+    using R = Ring<En::KW, En::RB, En::kStages, SOLO>;
+    constexpr int kStages = En::kStages;
     using E = typename En::E;
     static_assert(R::kStage >= En::kRows * D * 4, "a stage holds a warp's accumulator");
     float *own = reinterpret_cast<float *>(smem + kAttnWarps * R::kBytes);
@@ -753,16 +795,25 @@ __device__ __forceinline__ void join_head(const AttnArgs &a) {
     }
     if (ch == 0) s_l[grp] = l;
     s_o[grp][ch] = x;
-    __syncthreads();
-    if (tid >= kLanes) return;
-    l = 0.f;
-    x = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-    for (int i = 0; i < kGroups; ++i) {
-        const float4 w = s_o[i][tid];
-        l += s_l[i];
-        x.x += w.x; x.y += w.y; x.z += w.z; x.w += w.w;
+    // the groups' sums: 8 (kSome) groups take what the others have, then one
+    constexpr int kSome = kGroups < 8 ? kGroups : 8;
+    for (int left = kGroups, to = kSome; left > 1; left = to, to = 1) {
+        __syncthreads();
+        if (grp < to) {
+            for (int i = grp + to; i < left; i += to) {
+                const float4 w = s_o[i][ch];
+                l += s_l[i];
+                x.x += w.x; x.y += w.y; x.z += w.z; x.w += w.w;
+            }
+        }
+        __syncthreads();
+        if (grp < to) {
+            if (ch == 0) s_l[grp] = l;
+            s_o[grp][ch] = x;
+        }
+        if (to == 1) break;
     }
+    if (tid >= kLanes) return;
     write_result(a, o + tid * 4, hd, tid == 0, m, l, x);
 }
 

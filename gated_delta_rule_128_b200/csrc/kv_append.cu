@@ -21,6 +21,16 @@ __device__ __forceinline__ bool table_ok(const int *cu, int N, int T) {
     return !__syncthreads_or(bad);
 }
 
+// the lengths with the new tokens (`ok`: cu is as it should be)
+__device__ __forceinline__ void write_lens(const PagedView &c, const int *cu, bool ok, int *lens_out, unsigned int *status) {
+    for (int n = threadIdx.x; n < c.N; n += blockDim.x) {
+        const int len = c.lens[n], count = ok ? cu[n + 1] - cu[n] : 0;
+        const bool fits = len >= 0 && len <= c.cap - count;
+        if (!fits) record_status(status, GDN2_ERR_INVALID_ARG);
+        lens_out[n] = fits ? len + count : len;
+    }
+}
+
 // Block b copies tokens [b per, b per + per).  Its first threads find each
 // token's place (packed: a binary search in cu); then all threads copy 16-byte
 // pieces, consecutive threads consecutive pieces of one token.
@@ -34,6 +44,7 @@ kv_append_kernel(const PagedView c, const uint4 *k, const uint4 *v, const int *c
     wait_for_previous();
     if (cu && !table_ok(cu, c.N, T)) {
         if (tid == 0) record_status(status, GDN2_ERR_INVALID_ARG);
+        if (lens_out != c.lens && blockIdx.x == 0) write_lens(c, cu, false, lens_out, status);
         return;
     }
     if (tid < nt) {
@@ -63,6 +74,8 @@ kv_append_kernel(const PagedView c, const uint4 *k, const uint4 *v, const int *c
         // one token a sequence: no other block reads this length
         if (!cu) lens_out[n] = fits ? len + 1 : len;
     }
+    // packed, and the new lengths go to a place of their own: block 0 writes them
+    if (cu && lens_out != c.lens && blockIdx.x == 0) write_lens(c, cu, true, lens_out, status);
     __syncthreads();
     const int rv = c.d * c.es / 16, tv = c.Hkv * rv;  // 16-byte pieces of a row, of a token
     for (long long x = tid; x < (long long)nt * tv; x += kAppThreads) {
@@ -81,20 +94,15 @@ kv_append_kernel(const PagedView c, const uint4 *k, const uint4 *v, const int *c
         }
 }
 
-// The lengths after a packed append, once its rows are written (in place, the
-// copy above still reads the old ones).
+// In place, the lengths after a packed append wait until its rows are written:
+// the copy still reads the old ones.  (And without new tokens there is no copy.)
 __global__ void __launch_bounds__(1024)
 kv_lens_kernel(const PagedView c, const int *cu, int T, int *lens_out, unsigned int *status) {
     allow_next_launch();
     wait_for_previous();
     const bool ok = table_ok(cu, c.N, T);
     if (!ok && threadIdx.x == 0) record_status(status, GDN2_ERR_INVALID_ARG);
-    for (int n = threadIdx.x; n < c.N; n += blockDim.x) {
-        const int len = c.lens[n], count = ok ? cu[n + 1] - cu[n] : 0;
-        const bool fits = len >= 0 && len <= c.cap - count;
-        if (!fits) record_status(status, GDN2_ERR_INVALID_ARG);
-        lens_out[n] = fits ? len + count : len;
-    }
+    write_lens(c, cu, ok, lens_out, status);
 }
 
 cudaError_t kv_append_launch(const PagedView &c, const void *k, const void *v, const int *cu, int T,
@@ -107,7 +115,9 @@ cudaError_t kv_append_launch(const PagedView &c, const void *k, const void *v, c
                                             lens_out, status);
         if (e != cudaSuccess) return e;
     }
-    return cu ? launch_behind(K_KV_LENS, kv_lens_kernel, 1, 1024, 0, s, c, cu, T, lens_out, status) : cudaSuccess;
+    return cu && (T == 0 || lens_out == c.lens)
+               ? launch_behind(K_KV_LENS, kv_lens_kernel, 1, 1024, 0, s, c, cu, T, lens_out, status)
+               : cudaSuccess;
 }
 
 }  // namespace gdn2
