@@ -115,7 +115,7 @@ gdn2_status gdn2_attn_decode_step(const gdn2_paged_kv *kv, const void *q, void *
 
 size_t gdn2_kv_evict_workspace_bytes(const gdn2_paged_kv *kv, int budget) {
     PagedView c;
-    if (make_view(c, kv) != GDN2_OK || budget < 1) return 0;
+    if (make_view(c, kv) != GDN2_OK || budget < 1 || !evict_countable(c, budget)) return 0;
     return evict_ws_bytes(c, budget);
 }
 
@@ -132,6 +132,7 @@ gdn2_status gdn2_kv_evict(const gdn2_paged_kv *kv, const gdn2_paged_kv *dst, int
     }
     if (!c.w || budget < 1 || sink < 0 || recent < 0 || (long long)sink + recent > budget || !aligned(kept, 4))
         return GDN2_ERR_INVALID_ARG;
+    if (!evict_countable(c, budget)) return GDN2_ERR_UNSUPPORTED;
     if (!ws || !aligned(ws, 16) || ws_bytes < evict_ws_bytes(c, budget)) return GDN2_ERR_WORKSPACE;
     unsigned int *status = status_word();
     if (!status) return GDN2_ERR_CUDA;

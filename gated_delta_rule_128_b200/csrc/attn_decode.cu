@@ -666,8 +666,7 @@ attn_split_kernel(const AttnArgs a) {
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const PagedView &c = a.c;
     const int per = c.Hkv * a.HB;
-    allow_next_launch();
-    wait_for_previous();
+    follow_previous();
     Run run;
     if constexpr (SOLO) {
         run.n = blockIdx.x / per;
@@ -754,11 +753,11 @@ __device__ __forceinline__ void join_head(const AttnArgs &a) {
     const int hb = g / a.hpb, row = g - hb * a.hpb;
     const size_t hd = blockIdx.x;
     E *o = static_cast<E *>(a.o) + hd * D;
+    const int2 pr = a.parts[((size_t)n * a.c.Hkv + kvh) * a.HB + hb];  // means nothing for an empty sequence
     if (checked_len(a.c, n, a.status) == 0) {
         if (tid < kLanes) write_result(a, o + tid * 4, hd, tid == 0, -INFINITY, 0.f, make_float4(0.f, 0.f, 0.f, 0.f));
         return;
     }
-    const int2 pr = a.parts[((size_t)n * a.c.Hkv + kvh) * a.HB + hb];
     if (pr.x < 0) return;
     const int grp = tid / kLanes, ch = tid - grp * kLanes;
     float4 v[kAhead];
@@ -860,14 +859,22 @@ __device__ __forceinline__ void add_weights(const AttnArgs &a, int first_block) 
             if (lane == 0) s_L[g] = L;
         }
         __syncthreads();
-        for (int t = t0 + sub; t < t0 + cnt; t += NT / kUnit) {
-            const int j = first + t * kUnit + tok;
-            if (j >= len) continue;
-            int entry, slot;
-            page_slot(c, j, entry, slot);
-            const int page = page_of(c, run.n, entry);
-            if (page < 0) continue;
-            float sum = 0.f;
+        constexpr int kStep = NT / kUnit, kAhead = 2;  // units at once, and a thread's whose loads go out together
+        for (int t = t0 + sub; t < t0 + cnt; t += kAhead * kStep) {
+            int page[kAhead], slot[kAhead], at[kAhead];
+            float sum[kAhead];
+#pragma unroll
+            for (int u = 0; u < kAhead; ++u) {
+                const int j = first + (t + u * kStep) * kUnit + tok;
+                page[u] = -1;
+                sum[u] = 0.f;
+                at[u] = 0;  // what is not wanted reads unit t's, without a branch
+                if (t + u * kStep >= t0 + cnt || j >= len) continue;
+                at[u] = u * kStep * a.hpb * kUnit;
+                int entry;
+                page_slot(c, j, entry, slot[u]);
+                page[u] = page_of(c, run.n, entry);
+            }
             for (int hb = 0; hb < a.HB; ++hb) {
                 // the split kernel's number of this unit: it has Hkv HB runs a sequence
                 const int run_of = h * a.HB + hb;
@@ -878,10 +885,16 @@ __device__ __forceinline__ void add_weights(const AttnArgs &a, int first_block) 
 #pragma unroll 4
                 for (int r = 0; r < rows; ++r) {
                     const float L = s_L[hb * a.hpb + r];
-                    sum += L == -INFINITY ? 0.f : exp2f(s[r * kUnit] - L);
+#pragma unroll
+                    for (int u = 0; u < kAhead; ++u) {
+                        const float e = exp2f(s[at[u] + r * kUnit] - L);
+                        sum[u] += L == -INFINITY ? 0.f : e;
+                    }
                 }
             }
-            atomicAdd(c.w + weight_off(c, page, slot, h), sum);
+#pragma unroll
+            for (int u = 0; u < kAhead; ++u)
+                if (page[u] >= 0) atomicAdd(c.w + weight_off(c, page[u], slot[u], h), sum[u]);
         }
         run.u += cnt;
         if (run.u == run.base + c.Hkv * T) {
@@ -894,8 +907,7 @@ __device__ __forceinline__ void add_weights(const AttnArgs &a, int first_block) 
 template <typename E, int D, int NT, bool SOLO>
 __global__ void __launch_bounds__(NT)
 attn_finish_kernel(const AttnArgs a) {
-    allow_next_launch();
-    wait_for_previous();
+    follow_previous();
     const int heads = SOLO ? 0 : a.c.N * a.H;
     if (!SOLO && blockIdx.x < heads) join_head<E, D, NT>(a);
     else add_weights<NT, SOLO>(a, heads);
@@ -956,7 +968,7 @@ static cudaError_t attn_run_as(const AttnArgs &a, cudaStream_t s) {
     if (heads <= sm_count())
         return launch_behind(K_ATTN_FINISH, attn_finish_kernel<E, D, 1024, SOLO>, (SOLO ? 0 : heads) + (a.scores ? 2 * sm_count() : 0),
                              1024, 0, s, a);
-    return launch_behind(K_ATTN_FINISH, attn_finish_kernel<E, D, 128, SOLO>, (SOLO ? 0 : heads) + (a.scores ? 12 * sm_count() : 0),
+    return launch_behind(K_ATTN_FINISH, attn_finish_kernel<E, D, 128, SOLO>, (SOLO ? 0 : heads) + (a.scores ? 8 * sm_count() : 0),
                          128, 0, s, a);
 }
 template <class En, int D>

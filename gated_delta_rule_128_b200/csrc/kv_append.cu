@@ -40,8 +40,7 @@ kv_append_kernel(const PagedView c, const uint4 *k, const uint4 *v, const int *c
     __shared__ long long s_off[kAppTokens];  // byte offset of head 0's row, -1: not written
     __shared__ size_t s_w[kAppTokens];
     const int t0 = blockIdx.x * per, nt = min(per, T - t0), tid = threadIdx.x;
-    allow_next_launch();
-    wait_for_previous();
+    follow_previous();
     if (cu && !table_ok(cu, c.N, T)) {
         if (tid == 0) record_status(status, GDN2_ERR_INVALID_ARG);
         if (lens_out != c.lens && blockIdx.x == 0) write_lens(c, cu, false, lens_out, status);
@@ -98,8 +97,7 @@ kv_append_kernel(const PagedView c, const uint4 *k, const uint4 *v, const int *c
 // the copy still reads the old ones.  (And without new tokens there is no copy.)
 __global__ void __launch_bounds__(1024)
 kv_lens_kernel(const PagedView c, const int *cu, int T, int *lens_out, unsigned int *status) {
-    allow_next_launch();
-    wait_for_previous();
+    follow_previous();
     const bool ok = table_ok(cu, c.N, T);
     if (!ok && threadIdx.x == 0) record_status(status, GDN2_ERR_INVALID_ARG);
     write_lens(c, cu, ok, lens_out, status);

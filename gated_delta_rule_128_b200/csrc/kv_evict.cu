@@ -28,6 +28,17 @@ constexpr int kMostRanks = 16;     // blocks of a cluster
 constexpr int kMaxKeys = 40960;    // keys of a block's slice in shared memory
 constexpr int kMoveThreads = 256;
 
+constexpr long long kWaitClocks = 4000000000LL;
+
+__device__ __forceinline__ int ld_acquire(const int *p) {
+    int x;
+    asm volatile("ld.acquire.gpu.global.s32 %0, [%1];" : "=r"(x) : "l"(p) : "memory");
+    return x;
+}
+__device__ __forceinline__ void st_release(int *p, int x) {
+    asm volatile("st.release.gpu.global.s32 [%0], %1;" ::"l"(p), "r"(x) : "memory");
+}
+
 struct EvictPlan {
     int first, count;  // rows [first, count) move; count < 0: nothing, the length included
 };
@@ -73,11 +84,12 @@ __device__ __forceinline__ int block_scan(int x, int *warp_tot) {
 }
 
 // Block (n h, rank) of a cluster.  slots: the keys that dynamic shared memory
-// holds; stride: entries of a list.
+// holds; stride: entries of a list; flags: evict_shift's, one a chunk of each
+// list and the ticket behind them, or nullptr.
 template <int NT>
 __global__ void __launch_bounds__(NT)
 evict_select_kernel(const PagedView c, const PagedView to, int in_place, int budget, int sink, int recent,
-                    int slots, int stride, int *list_all, EvictPlan *plan, unsigned int *status) {
+                    int slots, int stride, int *list_all, EvictPlan *plan, int *flags, int chunks, unsigned int *status) {
     constexpr int kWarps = NT / 32, kOwn = kBins / NT;  // digits of a thread
     extern __shared__ unsigned s_key[];
     __shared__ __align__(16) int hist[kDigits][kBins];
@@ -90,8 +102,11 @@ evict_select_kernel(const PagedView c, const PagedView to, int in_place, int bud
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int nh = blockIdx.x / ranks, n = nh / c.Hkv, h = nh - n * c.Hkv;
     int *list = list_all + (size_t)nh * stride;
-    allow_next_launch();
-    wait_for_previous();
+    follow_previous();
+    if (flags) {  // for evict_shift: no chunk read, no ticket taken
+        for (int j = rank * NT + tid; j < chunks; j += ranks * NT) flags[(size_t)nh * chunks + j] = 0;
+        if (blockIdx.x == 0 && tid == 0) flags[(size_t)c.N * c.Hkv * chunks] = 0;
+    }
     const int raw = c.lens[n];
     int len = checked_len(c, n, status);
     if (min(len, budget) > to.cap) {
@@ -249,8 +264,8 @@ evict_select_kernel(const PagedView c, const PagedView to, int in_place, int bud
 // of one (sequence, head), a thread carrying the same 16-byte piece of kDeep
 // rows of k and of v; the next item's places are looked up (list, then tables)
 // while this one's rows are on their way.  The weights are items of their own.
-constexpr int kDeep = 4;
-constexpr int kCopyBlocksPerSm = 3;
+constexpr int kDeep = 2;
+constexpr int kCopyBlocksPerSm = 4;
 __global__ void __launch_bounds__(kMoveThreads, kCopyBlocksPerSm)
 evict_copy_kernel(const PagedView c, const PagedView to, int stride, int chunks, int wchunks, const int *list_all,
                   const EvictPlan *plan, unsigned int *status) {
@@ -258,8 +273,7 @@ evict_copy_kernel(const PagedView c, const PagedView to, int stride, int chunks,
     const int piece = threadIdx.x % pieces, r = threadIdx.x / pieces;
     const long long rows = (long long)c.N * c.Hkv * chunks, total = rows + (long long)c.N * c.Hkv * wchunks;
     long long from[kDeep], dst[kDeep];
-    allow_next_launch();
-    wait_for_previous();
+    follow_previous();
     // the places of row i0 + u step, u < kDeep, of (sequence, head) nh; -1: not written
     auto places = [&](int nh, long long i0, int step, auto place) {
         const int n = nh / c.Hkv, h = nh - n * c.Hkv, count = plan[nh].count;
@@ -286,7 +300,9 @@ evict_copy_kernel(const PagedView c, const PagedView to, int stride, int chunks,
         }
     };
     auto row_places = [&](long long x) {
-        const int nh = (int)(x / chunks), chunk = (int)(x - (long long)nh * chunks);
+        // heads first: blocks at work at once then read and write the same pages
+        const long long y = x / c.Hkv;
+        const int n = (int)(y / chunks), chunk = (int)(y - (long long)n * chunks), nh = n * c.Hkv + (int)(x - y * c.Hkv);
         places(nh, (long long)chunk * at_once * kDeep + r, at_once, [&](int u, int pg, int sl, int pg2, int sl2, int h) {
             from[u] = row_off(c, pg, sl, h) + piece * 16;
             dst[u] = row_off(to, pg2, sl2, h) + piece * 16;
@@ -330,127 +346,154 @@ evict_copy_kernel(const PagedView c, const PagedView to, int stride, int chunks,
     }
 }
 
-// In place.  Block (n h, column): 16 LANES bytes of every row of k or of v, the
-// kept tokens in order, a batch ahead in registers.  Row i is read from
-// list[i] >= i, so a batch overwrites only rows that it or earlier batches
-// have read, and columns need no agreement between blocks.  The fewer
-// (sequence, head) pairs there are, the narrower the columns, to have blocks.
-constexpr int kBatch = 8;
-template <int LANES>
-__global__ void __launch_bounds__(kMoveThreads)
-evict_shift_kernel(const PagedView c, int stride, const int *list_all, const EvictPlan *plan, unsigned int *status) {
-    constexpr int kStep = kMoveThreads / LANES;
-    const int columns = c.d * c.es / (16 * LANES);
-    const int nh = blockIdx.x / (2 * columns), col = blockIdx.x % (2 * columns);
-    const int n = nh / c.Hkv, h = nh - n * c.Hkv;
-    allow_next_launch();
-    wait_for_previous();
-    const EvictPlan p = plan[nh];
-    const int *list = list_all + (size_t)nh * stride;
-    const int lane = threadIdx.x % LANES, r = threadIdx.x / LANES;
-    char *pool = (col < columns ? c.k : c.v) + (size_t)(col % columns) * (16 * LANES) + lane * 16;
-    const bool weights = col == 0 && lane == 0;
-    uint4 x[kBatch], x2[kBatch];
-    float w[kBatch], w2[kBatch];
-    unsigned ok = 0, ok2 = 0;
-    auto load = [&](int i0, uint4 *y, float *wy, unsigned &have) {
-        have = 0;
+// In place, where a row may overwrite one that is still to be read.  Chunks of
+// rows are taken in the order of a ticket: chunk by chunk, in each the
+// (sequence, head)s.  A block reads its chunk, says so in the chunk's flag, and
+// writes it once every earlier chunk of that (sequence, head) has been read:
+// row i comes from list[i] >= i, so the rows that chunk x overwrites belong to
+// chunks up to x.  No block waits before it has read its own chunk, and it
+// waits for blocks with earlier tickets only, which are at work already, so
+// every wait ends whichever blocks the GPU runs; it gives up all the same
+// after some seconds (GDN2_ERR_TIMEOUT).
+__global__ void __launch_bounds__(kMoveThreads, kCopyBlocksPerSm)
+evict_shift_kernel(const PagedView c, int stride, int chunks, const int *list_all, const EvictPlan *plan, int *flags,
+                   int *ticket, unsigned int *status) {
+    __shared__ int s_ticket;
+    const int pieces = c.d * c.es / 16, at_once = kMoveThreads / pieces, nhs = c.N * c.Hkv;
+    const int piece = threadIdx.x % pieces, r = threadIdx.x / pieces;
+    const long long total = (long long)nhs * chunks;
+    follow_previous();
+    for (;;) {
+        __syncthreads();  // the last ticket has been read
+        if (threadIdx.x == 0) s_ticket = atomicAdd(ticket, 1);
+        __syncthreads();
+        const long long x = (unsigned)s_ticket;
+        if (x >= total) return;
+        const int chunk = (int)(x / nhs), nh = (int)(x - (long long)chunk * nhs), n = nh / c.Hkv, h = nh - n * c.Hkv;
+        const EvictPlan p = plan[nh];
+        if (h == 0 && chunk == 0 && threadIdx.x == 0 && p.count >= 0) c.lens[n] = p.count;
+        const long long i0 = p.first + (long long)chunk * at_once * kDeep;
+        if (i0 >= p.count) continue;
+        const int *list = list_all + (size_t)nh * stride;
+        int *flag = flags + (size_t)nh * chunks;
+        uint4 k[kDeep], v[kDeep];
+        float w[kDeep];
+        int src[kDeep], page[kDeep], slot[kDeep];
 #pragma unroll
-        for (int u = 0; u < kBatch; ++u) {
-            const int i = i0 + u * kStep + r;
-            if (i >= p.count) continue;
-            int entry, slot;
-            page_slot(c, list[i], entry, slot);
-            const int page = page_of(c, n, entry);
-            if (page < 0) {
+        for (int u = 0; u < kDeep; ++u) {
+            const long long i = i0 + r + u * at_once;
+            src[u] = i < p.count ? list[i] : -1;
+        }
+#pragma unroll
+        for (int u = 0; u < kDeep; ++u) {
+            page[u] = -1;
+            if (src[u] < 0) continue;
+            int entry;
+            page_slot(c, src[u], entry, slot[u]);
+            page[u] = page_of(c, n, entry);
+            if (page[u] < 0) record_status(status, GDN2_ERR_INVALID_ARG);
+        }
+#pragma unroll
+        for (int u = 0; u < kDeep; ++u) {
+            if (page[u] < 0) continue;
+            const long long at = row_off(c, page[u], slot[u], h) + piece * 16;
+            k[u] = *reinterpret_cast<const uint4 *>(c.k + at);
+            v[u] = *reinterpret_cast<const uint4 *>(c.v + at);
+            if (piece == 0) w[u] = c.w[weight_off(c, page[u], slot[u], h)];
+        }
+        __syncthreads();
+        if (threadIdx.x == 0) {
+            __threadfence();
+            st_release(flag + chunk, 1);
+        }
+        bool ready = true;
+        for (int j = threadIdx.x; j < chunk && ready; j += kMoveThreads) {
+            if (ld_acquire(flag + j)) continue;
+            const long long t0 = clock64();
+            while (!ld_acquire(flag + j) && ready) ready = clock64() - t0 < kWaitClocks;
+        }
+        if (!__syncthreads_and(ready)) {
+            if (threadIdx.x == 0) record_status(status, GDN2_ERR_TIMEOUT);
+            continue;
+        }
+#pragma unroll
+        for (int u = 0; u < kDeep; ++u) {
+            if (page[u] < 0) continue;
+            int entry, to_slot;
+            page_slot(c, (int)(i0 + r + u * at_once), entry, to_slot);
+            const int to_page = page_of(c, n, entry);
+            if (to_page < 0) {
                 record_status(status, GDN2_ERR_INVALID_ARG);
                 continue;
             }
-            y[u] = *reinterpret_cast<const uint4 *>(pool + row_off(c, page, slot, h));
-            if (weights) wy[u] = c.w[weight_off(c, page, slot, h)];
-            have |= 1u << u;
+            const long long at = row_off(c, to_page, to_slot, h) + piece * 16;
+            *reinterpret_cast<uint4 *>(c.k + at) = k[u];
+            *reinterpret_cast<uint4 *>(c.v + at) = v[u];
+            if (piece == 0) c.w[weight_off(c, to_page, to_slot, h)] = w[u];
         }
-    };
-    load(p.first, x, w, ok);
-    for (int i0 = p.first; i0 < p.count; i0 += kStep * kBatch) {
-        if (i0 + kStep * kBatch < p.count) load(i0 + kStep * kBatch, x2, w2, ok2);
-        else ok2 = 0;
-        __syncthreads();  // the block has read this batch and the next before it writes
-#pragma unroll
-        for (int u = 0; u < kBatch; ++u) {
-            if (!(ok >> u & 1u)) continue;
-            int entry, slot;
-            page_slot(c, i0 + u * kStep + r, entry, slot);
-            const int page = page_of(c, n, entry);
-            if (page < 0) {
-                record_status(status, GDN2_ERR_INVALID_ARG);
-                continue;
-            }
-            *reinterpret_cast<uint4 *>(pool + row_off(c, page, slot, h)) = x[u];
-            if (weights) c.w[weight_off(c, page, slot, h)] = w[u];
-        }
-#pragma unroll
-        for (int u = 0; u < kBatch; ++u) {
-            x[u] = x2[u];
-            w[u] = w2[u];
-        }
-        ok = ok2;
     }
-    if (h == 0 && col == 0 && threadIdx.x == 0 && p.count >= 0) c.lens[n] = p.count;
 }
 
 // entries of a list in the workspace
 static int list_stride(const PagedView &c, int budget) { return budget < c.cap ? budget : c.cap; }
 
-size_t evict_ws_bytes(const PagedView &c, int budget) {
-    const size_t nh = (size_t)c.N * c.Hkv;
-    return align256(nh * sizeof(EvictPlan)) + align256(nh * list_stride(c, budget) * sizeof(int));
+// rows of a chunk, and chunks of a list
+static int chunk_rows(const PagedView &c) { return kMoveThreads / (c.d * c.es / 16) * kDeep; }
+static int chunk_count(const PagedView &c, int stride) { return (stride + chunk_rows(c) - 1) / chunk_rows(c); }
+
+// chunks that the tickets may have to count
+bool evict_countable(const PagedView &c, int budget) {
+    return (long long)c.N * c.Hkv * chunk_count(c, list_stride(c, budget)) < 1LL << 30;
 }
 
-template <int LANES>
-static cudaError_t shift_launch(const PagedView &c, int stride, const int *list, const EvictPlan *plan,
-                                unsigned int *status, cudaStream_t s) {
-    return launch_behind(K_EVICT_MOVE, evict_shift_kernel<LANES>, c.N * c.Hkv * 2 * (c.d * c.es / (16 * LANES)),
-                         kMoveThreads, 0, s, c, stride, list, plan, status);
+size_t evict_ws_bytes(const PagedView &c, int budget) {
+    const size_t nh = (size_t)c.N * c.Hkv;
+    const int stride = list_stride(c, budget);
+    return align256(nh * sizeof(EvictPlan)) + align256(nh * stride * sizeof(int)) +
+           align256((nh * chunk_count(c, stride) + 1) * sizeof(int));
 }
 
 template <int NT>
 static cudaError_t select_launch(const PagedView &src, const PagedView &dst, bool in_place, int budget, int sink, int recent,
-                                 int ranks, int slots, int stride, int *list, EvictPlan *plan, unsigned int *status,
-                                 cudaStream_t s) {
+                                 int ranks, int slots, int stride, int *list, EvictPlan *plan, int *flags, int chunks,
+                                 unsigned int *status, cudaStream_t s) {
     const auto kernel = evict_select_kernel<NT>;
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxKeys * 4);
-    if (e == cudaSuccess) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    cudaError_t e = cudaSuccess;
+    if (slots * 4 > 16 << 10)  // with the static arrays above what any kernel may have
+        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxKeys * 4);
+    if (e == cudaSuccess && ranks > 8) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
     if (e != cudaSuccess) return e;
     return launch_clusters(K_EVICT_SELECT, kernel, ranks, src.N * src.Hkv * ranks, NT, slots * 4, s, src, dst, (int)in_place,
-                           budget, sink, recent, slots, stride, list, plan, status);
+                           budget, sink, recent, slots, stride, list, plan, flags, chunks, status);
 }
 
 cudaError_t evict_launch(const PagedView &src, const PagedView &dst, bool in_place, int budget, int sink,
                          int recent, int *kept, void *ws, unsigned int *status, cudaStream_t s) {
     const int nh = src.N * src.Hkv;
     EvictPlan *plan = static_cast<EvictPlan *>(ws);
-    const int stride = kept ? budget : list_stride(src, budget);
-    int *list = kept ? kept : at<int>(ws, align256((size_t)nh * sizeof(EvictPlan)));
+    const int stride = kept ? budget : list_stride(src, budget);  // entries of a list
+    const int own = list_stride(src, budget), chunks = chunk_count(src, own);
+    int *const own_list = at<int>(ws, align256((size_t)nh * sizeof(EvictPlan)));
+    int *list = kept ? kept : own_list;
+    int *flags = at<int>(own_list, align256((size_t)nh * own * sizeof(int)));
     // blocks of a cluster: until a slice is 4096 tokens or the GPU is full
     int ranks = 1;
     while (ranks < kMostRanks && src.cap / ranks > 4096 && (long long)nh * ranks < sm_count()) ranks *= 2;
     const int slice = (int)(((long long)src.cap + ranks - 1) / ranks), slots = slice < kMaxKeys ? slice : kMaxKeys;
     // one block an SM has 1024 threads; several hide each other's waits with 512
     cudaError_t e = (long long)nh * ranks <= sm_count()
-                        ? select_launch<1024>(src, dst, in_place, budget, sink, recent, ranks, slots, stride, list, plan, status, s)
-                        : select_launch<512>(src, dst, in_place, budget, sink, recent, ranks, slots, stride, list, plan, status, s);
+                        ? select_launch<1024>(src, dst, in_place, budget, sink, recent, ranks, slots, stride, list, plan, in_place ? flags : nullptr, chunks, status, s)
+                        : select_launch<512>(src, dst, in_place, budget, sink, recent, ranks, slots, stride, list, plan, in_place ? flags : nullptr, chunks, status, s);
     if (e != cudaSuccess) return e;
+    const long long blocks = (long long)kCopyBlocksPerSm * sm_count();
     if (in_place) {
-        const long long narrow = (long long)nh * 2 * (src.d * src.es / 16);  // blocks of 16-byte columns
-        if (narrow >= 16LL * sm_count()) return shift_launch<4>(src, stride, list, plan, status, s);
-        if (narrow >= 4LL * sm_count()) return shift_launch<2>(src, stride, list, plan, status, s);
-        return shift_launch<1>(src, stride, list, plan, status, s);
+        const long long items = (long long)nh * chunks;
+        return launch_behind(K_EVICT_MOVE, evict_shift_kernel, (int)(items < blocks ? items : blocks), kMoveThreads, 0, s,
+                             src, stride, chunks, list, plan, flags, flags + (size_t)nh * chunks, status);
     }
-    const int rows = kMoveThreads / (src.d * src.es / 16) * kDeep, chunks = (stride + rows - 1) / rows;
     const int wchunks = (stride + kMoveThreads * kDeep - 1) / (kMoveThreads * kDeep);
-    const long long items = (long long)nh * (chunks + wchunks), most = (long long)kCopyBlocksPerSm * sm_count();
-    return launch_behind(K_EVICT_MOVE, evict_copy_kernel, (int)(items < most ? items : most), kMoveThreads, 0, s, src,
+    const long long items = (long long)nh * (chunks + wchunks);
+    return launch_behind(K_EVICT_MOVE, evict_copy_kernel, (int)(items < blocks ? items : blocks), kMoveThreads, 0, s, src,
                          dst, stride, chunks, wchunks, list, plan, status);
 }
 

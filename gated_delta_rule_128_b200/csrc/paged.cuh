@@ -48,12 +48,15 @@ __device__ __forceinline__ int checked_len(const PagedView &c, int n, unsigned i
     return 0;
 }
 
-// The kernels of one call follow each other on the stream without waiting for
-// the launch: a kernel allows the next one's blocks to come up at once, and
-// those wait, before their first access, until it has finished.
-__device__ __forceinline__ void allow_next_launch() { asm volatile("griddepcontrol.launch_dependents;"); }
-__device__ __forceinline__ void wait_for_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
-
+// The kernels here follow each other on the stream without the launch between
+// them: every kernel first waits until the one before it has finished and its
+// writes are visible, whatever kernel that is, and then lets the next one's
+// blocks come up, which wait in their turn.  Called by every thread, before
+// any access to global memory.
+__device__ __forceinline__ void follow_previous() {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;");
+}
 // launches a kernel whose blocks come up while the one before it still runs
 // (they wait for it themselves), in clusters of `ranks` blocks
 template <typename... P, typename... A>
@@ -88,6 +91,7 @@ bool attn_countable(const PagedView &c, int H);
 size_t attn_ws_bytes(const PagedView &c, int H, int add_weights);
 cudaError_t attn_launch(const PagedView &c, const void *q, void *o, float *lse, int H, float scale,
                         int window, int add_weights, void *ws, unsigned int *status, cudaStream_t s);
+bool evict_countable(const PagedView &c, int budget);
 size_t evict_ws_bytes(const PagedView &c, int budget);
 cudaError_t evict_launch(const PagedView &src, const PagedView &dst, bool in_place, int budget, int sink,
                          int recent, int *kept, void *ws, unsigned int *status, cudaStream_t s);

@@ -257,7 +257,7 @@ gdn2_status gdn2_bwd_varlen(const void *q, const void *k, const void *v, const v
  * it leave that page's tokens out; either records GDN2_ERR_INVALID_ARG in the
  * device status word.  No access leaves the pools.
  * Sequences may share pages (a common prompt) in every call that only reads
- * them; a page that a call writes must belong to one sequence. */
+ * them; a page that a call writes must belong to one sequence, once. */
 typedef struct {
     void *k, *v;
     float *weight;
@@ -326,8 +326,8 @@ size_t gdn2_kv_evict_workspace_bytes(const gdn2_paged_kv *kv, int budget);
  *       kv is left as it is (for pages that sequences share).  dst->weight must
  *       be given; strides, page_size and max_pages may differ, dst must hold
  *       min(len, budget) tokens a sequence.
- *   budget >= 1; sink, recent >= 0; sink + recent <= budget.  kv->weight is
- *       needed.
+ *   budget >= 1; sink, recent >= 0; sink + recent <= budget; N * H_kv *
+ *       min(budget, max_pages * page_size) < 2^33.  kv->weight is needed.
  *   kept : int32 [N, H_kv, budget], each new slot's former index (-1 behind the
  *       new length), or NULL. */
 gdn2_status gdn2_kv_evict(const gdn2_paged_kv *kv, const gdn2_paged_kv *dst, int budget, int sink,
