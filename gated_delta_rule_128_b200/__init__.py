@@ -581,6 +581,8 @@ def attn_decode_step(q, kv: PagedKV, *, scale: Optional[float] = None, window: i
         raise ValueError(f"q must have shape [N, H, d], got {tuple(q.shape)}")
     H = q.shape[1]
     _tensor("q", q, kv.k.dtype, (s.N, H, s.d), kv.device)
+    if not 0 <= window < 2 ** 31:
+        raise ValueError(f"window must be 0 or a number of tokens that fits 32 bits, got {window}")
     if o is not None:
         _tensor("o", o, q.dtype, q.shape, kv.device)
     with _on_stream(kv, stream):
@@ -606,8 +608,8 @@ def kv_evict(kv: PagedKV, budget: int, *, sink: int = 0, recent: int = 0, dst: O
     s = kv.struct
     if dst is not None and dst.device != kv.device:
         raise ValueError(f"dst is on {dst.device}, the cache on {kv.device}")
-    if budget < 1:
-        raise ValueError(f"budget must be at least 1, got {budget}")
+    if not (1 <= budget < 2 ** 31 and 0 <= sink <= budget and 0 <= recent <= budget - sink):
+        raise ValueError(f"budget must be at least 1 and sink + recent within it, got {budget}, {sink}, {recent}")
     with _on_stream(kv, stream):
         kept = torch.empty((s.N, s.H_kv, budget), dtype=torch.int32, device=kv.device) if want_kept else None
         ws = kv._workspace(ws, "gdn2_kv_evict_workspace_bytes", budget)

@@ -106,7 +106,7 @@ gdn2_status gdn2_attn_decode_step(const gdn2_paged_kv *kv, const void *q, void *
     if (st != GDN2_OK) return st;
     if ((st = check_heads(c, H)) != GDN2_OK) return st;
     if (!q || !o || !aligned(q, 16) || !aligned(o, 16) || !aligned(lse, 4)) return GDN2_ERR_INVALID_ARG;
-    if (window < 0 || !isfinite(scale) || (add_weights && !c.w)) return GDN2_ERR_INVALID_ARG;
+    if (window < 0 || !isfinite(scale * 1.5f)  /* with log2 e in it too */ || (add_weights && !c.w)) return GDN2_ERR_INVALID_ARG;
     if (!ws || !aligned(ws, 16) || ws_bytes < attn_ws_bytes(c, H, add_weights != 0)) return GDN2_ERR_WORKSPACE;
     unsigned int *status = status_word();
     if (!status) return GDN2_ERR_CUDA;

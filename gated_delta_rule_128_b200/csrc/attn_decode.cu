@@ -55,7 +55,8 @@ struct AttnArgs {
     float *part;        // [2 grid][kHeadBlock][d]
     int2 *parts;        // [N Hkv HB] first and last block with a part, or -1
     float *lse2;        // [N H] log-sum-exp in base 2 (for the weights), or nullptr
-    float *scores;      // [unit][hpb][kUnit] scores in base 2, or nullptr
+    float *scores;      // [score_units][hpb][kUnit] scores in base 2, or nullptr
+    int score_units;    // units whose scores are kept
     unsigned int *status;
 };
 
@@ -266,7 +267,7 @@ struct Ring {
         if (j < end) {
             int entry;
             page_slot(a.c, j, entry, slot);
-            page = __ldg(a.c.table + (size_t)n * a.c.max_pages + entry);
+            page = a.c.table[(size_t)n * a.c.max_pages + entry];
             head = h;
             token = true;
         }
@@ -694,7 +695,7 @@ attn_split_kernel(const AttnArgs a) {
             cp_async_wait<kStages - 1>();
             __syncwarp();
             const int tok = (i * kAttnWarps + warp) * En::KW;  // in the segment
-            float *sc = a.scores ? a.scores + (size_t)(sg.unit + tok / kUnit) * a.hpb * kUnit + tok % kUnit : nullptr;
+            float *sc = a.scores && sg.unit + tok / kUnit < a.score_units ? a.scores + (size_t)(sg.unit + tok / kUnit) * a.hpb * kUnit + tok % kUnit : nullptr;
             const uint32_t st = ring.base + stage * R::kStage;
             if (live) en.template step<R>(a, sg, st, st + R::kHalf, live, lane, sc, own);
             stage = stage == kStages - 1 ? 0 : stage + 1;
@@ -816,13 +817,26 @@ __device__ __forceinline__ void join_head(const AttnArgs &a) {
     write_result(a, o + tid * 4, hd, tid == 0, m, l, x);
 }
 
+// sum over `rows` query heads of 2^(s - lse) for one cached row
+template <typename E, int D>
+__device__ __noinline__ float weight_of_row(const AttnArgs &a, const E *q, const E *k, const float *L, int rows) {
+    float sum = 0.f;
+    for (int r = 0; r < rows; ++r) {
+        float s = 0.f;
+#pragma unroll 8
+        for (int i = 0; i < D; ++i) s = fmaf(ldx(q, r * D + i), ldx(k, i), s);
+        sum += L[r] == -INFINITY ? 0.f : exp2f(s * a.scale2 - L[r]);
+    }
+    return sum;
+}
+
 // The blocks behind those (first = N H; none unless weights are wanted):
 //   weight_j += sum over the group's heads of 2^(s_j - lse),
 // from the scores that the split kernel kept, 64 threads a unit, a token each.
 // A head's lse is the one written, or comes from its parts once more.  One
 // addition a token and call, so that no order matters unless sequences share
 // the page.
-template <int NT, bool SOLO>
+template <typename E, int D, int NT, bool SOLO>
 __device__ __forceinline__ void add_weights(const AttnArgs &a, int first_block) {
     __shared__ float s_L[kMostGroup];
     const PagedView &c = a.c;
@@ -882,6 +896,17 @@ __device__ __forceinline__ void add_weights(const AttnArgs &a, int first_block) 
                                       : run.base * a.HB + run_of * T + t;
                 const float *s = a.scores + (size_t)unit * a.hpb * kUnit + tok;
                 const int rows = min(a.hpb, a.G - hb * a.hpb);
+                if (unit - t + min(t + (kAhead - 1) * kStep, t0 + cnt - 1) >= a.score_units) {
+                    // past what was kept (sequences that share pages can hold more
+                    // tokens together than the pool): the scores once more
+#pragma unroll 1
+                    for (int u = 0; u < kAhead; ++u)
+                        if (page[u] >= 0)
+                            sum[u] += weight_of_row<E, D>(a, static_cast<const E *>(a.q) + ((size_t)run.n * a.H + h * a.G + hb * a.hpb) * D,
+                                                          reinterpret_cast<const E *>(c.k + row_off(c, page[u], slot[u], h)),
+                                                          s_L + hb * a.hpb, rows);
+                    continue;
+                }
 #pragma unroll 4
                 for (int r = 0; r < rows; ++r) {
                     const float L = s_L[hb * a.hpb + r];
@@ -910,7 +935,7 @@ attn_finish_kernel(const AttnArgs a) {
     follow_previous();
     const int heads = SOLO ? 0 : a.c.N * a.H;
     if (!SOLO && blockIdx.x < heads) join_head<E, D, NT>(a);
-    else add_weights<NT, SOLO>(a, heads);
+    else add_weights<E, D, NT, SOLO>(a, heads);
 }
 
 // ---- host side
@@ -925,6 +950,7 @@ static void head_blocks(const PagedView &c, int H, AttnArgs &a) {
 static size_t attn_ws(const PagedView &c, AttnArgs &a, int add_weights, void *ws) {
     a.ml = nullptr;
     a.part = a.lse2 = a.scores = nullptr;
+    a.score_units = 0;
     a.parts = nullptr;
     if (c.cap <= kSoloTokens && !add_weights) return 256;  // not touched
     const size_t slots = 2 * (size_t)kMostBlocksPerSm * sm_count(), runs = (size_t)c.N * c.Hkv * a.HB;
@@ -935,7 +961,12 @@ static size_t attn_ws(const PagedView &c, AttnArgs &a, int add_weights, void *ws
     a.parts = reinterpret_cast<int2 *>(take(runs * sizeof(int2)));
     if (add_weights) {
         a.lse2 = reinterpret_cast<float *>(take((size_t)c.N * a.H * sizeof(float)));
-        a.scores = reinterpret_cast<float *>(take(runs * ((c.cap + kUnit - 1) / kUnit) * a.hpb * kUnit * sizeof(float)));
+        // every unit there can be, or if that is less, as many as the pool has
+        // tokens for; a table much wider than the sequences costs nothing
+        const long long all = (long long)runs * ((c.cap + kUnit - 1) / kUnit);
+        const long long pool = ((long long)c.num_pages * c.page / kUnit + c.N) * c.Hkv * a.HB;
+        a.score_units = (int)(c.cap <= kSoloTokens || all < pool ? all : pool);
+        a.scores = reinterpret_cast<float *>(take((size_t)a.score_units * a.hpb * kUnit * sizeof(float)));
     }
     return o;
 }

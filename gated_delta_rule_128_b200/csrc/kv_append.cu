@@ -53,12 +53,12 @@ kv_append_kernel(const PagedView c, const uint4 *k, const uint4 *v, const int *c
             int lo = 0, hi = c.N;
             while (hi - lo > 1) {
                 const int mid = (lo + hi) >> 1;
-                if (__ldg(cu + mid) <= t) lo = mid;
+                if (cu[mid] <= t) lo = mid;
                 else hi = mid;
             }
             n = lo;
-            i = t - __ldg(cu + n);
-            count = __ldg(cu + n + 1) - __ldg(cu + n);
+            i = t - cu[n];
+            count = cu[n + 1] - cu[n];
         }
         const int len = c.lens[n];
         const bool fits = len >= 0 && len <= c.cap - count;

@@ -266,14 +266,41 @@ evict_select_kernel(const PagedView c, const PagedView to, int in_place, int bud
 // while this one's rows are on their way.  The weights are items of their own.
 constexpr int kDeep = 2;
 constexpr int kCopyBlocksPerSm = 4;
+
+// The most rows that any of the lists moves, for every thread of the block:
+// a budget may be far beyond what the sequences hold.
+__device__ __forceinline__ int most_rows(const EvictPlan *plan, int nhs) {
+    __shared__ int s_most[kMoveThreads / 32];
+    int most = 0;
+    for (int i = threadIdx.x; i < nhs; i += kMoveThreads) most = max(most, plan[i].count - plan[i].first);
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) most = max(most, __shfl_xor_sync(0xffffffffu, most, off));
+    if ((threadIdx.x & 31) == 0) s_most[threadIdx.x >> 5] = most;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < kMoveThreads / 32; ++w) most = max(most, s_most[w]);
+    return most;
+}
+// the new lengths, shared out over the grid
+__device__ __forceinline__ void write_lens(const PagedView &to, const EvictPlan *plan) {
+    for (int n = blockIdx.x * kMoveThreads + threadIdx.x; n < to.N; n += gridDim.x * kMoveThreads) {
+        const int count = plan[(size_t)n * to.Hkv].count;
+        if (count >= 0) to.lens[n] = count;
+    }
+}
 __global__ void __launch_bounds__(kMoveThreads, kCopyBlocksPerSm)
-evict_copy_kernel(const PagedView c, const PagedView to, int stride, int chunks, int wchunks, const int *list_all,
+evict_copy_kernel(const PagedView c, const PagedView to, int stride, const int *list_all,
                   const EvictPlan *plan, unsigned int *status) {
     const int pieces = c.d * c.es / 16, at_once = kMoveThreads / pieces;
     const int piece = threadIdx.x % pieces, r = threadIdx.x / pieces;
-    const long long rows = (long long)c.N * c.Hkv * chunks, total = rows + (long long)c.N * c.Hkv * wchunks;
     long long from[kDeep], dst[kDeep];
     follow_previous();
+    write_lens(to, plan);
+    const int most = most_rows(plan, c.N * c.Hkv);
+    if (most == 0) return;
+    const int chunks = (most + at_once * kDeep - 1) / (at_once * kDeep);
+    const int wchunks = (most + kMoveThreads * kDeep - 1) / (kMoveThreads * kDeep);
+    const long long rows = (long long)c.N * c.Hkv * chunks, total = rows + (long long)c.N * c.Hkv * wchunks;
     // the places of row i0 + u step, u < kDeep, of (sequence, head) nh; -1: not written
     auto places = [&](int nh, long long i0, int step, auto place) {
         const int n = nh / c.Hkv, h = nh - n * c.Hkv, count = plan[nh].count;
@@ -307,7 +334,6 @@ evict_copy_kernel(const PagedView c, const PagedView to, int stride, int chunks,
             from[u] = row_off(c, pg, sl, h) + piece * 16;
             dst[u] = row_off(to, pg2, sl2, h) + piece * 16;
         });
-        if (chunk == 0 && threadIdx.x == 0 && nh % c.Hkv == 0) to.lens[nh / c.Hkv] = plan[nh].count;
     };
     long long x = blockIdx.x;
     if (x < rows) row_places(x);
@@ -361,8 +387,10 @@ evict_shift_kernel(const PagedView c, int stride, int chunks, const int *list_al
     __shared__ int s_ticket;
     const int pieces = c.d * c.es / 16, at_once = kMoveThreads / pieces, nhs = c.N * c.Hkv;
     const int piece = threadIdx.x % pieces, r = threadIdx.x / pieces;
-    const long long total = (long long)nhs * chunks;
     follow_previous();
+    write_lens(c, plan);
+    const long long total = (long long)nhs * ((most_rows(plan, nhs) + at_once * kDeep - 1) / (at_once * kDeep));
+    if (total == 0) return;
     for (;;) {
         __syncthreads();  // the last ticket has been read
         if (threadIdx.x == 0) s_ticket = atomicAdd(ticket, 1);
@@ -371,7 +399,6 @@ evict_shift_kernel(const PagedView c, int stride, int chunks, const int *list_al
         if (x >= total) return;
         const int chunk = (int)(x / nhs), nh = (int)(x - (long long)chunk * nhs), n = nh / c.Hkv, h = nh - n * c.Hkv;
         const EvictPlan p = plan[nh];
-        if (h == 0 && chunk == 0 && threadIdx.x == 0 && p.count >= 0) c.lens[n] = p.count;
         const long long i0 = p.first + (long long)chunk * at_once * kDeep;
         if (i0 >= p.count) continue;
         const int *list = list_all + (size_t)nh * stride;
@@ -491,10 +518,9 @@ cudaError_t evict_launch(const PagedView &src, const PagedView &dst, bool in_pla
         return launch_behind(K_EVICT_MOVE, evict_shift_kernel, (int)(items < blocks ? items : blocks), kMoveThreads, 0, s,
                              src, stride, chunks, list, plan, flags, flags + (size_t)nh * chunks, status);
     }
-    const int wchunks = (stride + kMoveThreads * kDeep - 1) / (kMoveThreads * kDeep);
-    const long long items = (long long)nh * (chunks + wchunks);
+    const long long items = (long long)nh * (chunks + 1);
     return launch_behind(K_EVICT_MOVE, evict_copy_kernel, (int)(items < blocks ? items : blocks), kMoveThreads, 0, s, src,
-                         dst, stride, chunks, wchunks, list, plan, status);
+                         dst, stride, list, plan, status);
 }
 
 }  // namespace gdn2

@@ -31,7 +31,7 @@ __device__ __forceinline__ void page_slot(const PagedView &c, int j, int &entry,
 }
 // the page of table entry (n, entry), or -1 where the table names none
 __device__ __forceinline__ int page_of(const PagedView &c, int n, int entry) {
-    const int p = __ldg(c.table + (size_t)n * c.max_pages + entry);
+    const int p = c.table[(size_t)n * c.max_pages + entry];
     return (unsigned)p < (unsigned)c.num_pages ? p : -1;
 }
 __device__ __forceinline__ long long row_off(const PagedView &c, int page, int slot, int h) {

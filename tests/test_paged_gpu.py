@@ -192,6 +192,34 @@ def test_shared_pages_collect_every_sequences_weight(io):
     check(kv, c, q, q64, io, 0.2, 0, True)
 
 
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+@pytest.mark.parametrize("d,G", [(32, 1), (64, 5), (128, 20)])
+def test_a_long_prompt_shared_by_many_sequences(io, d, G):
+    """Together the sequences hold many times the tokens of the pool."""
+    N, lens = 30, 300
+    kv, c = cache([lens], 16, 2, d, io, 17, spare=0, fill=NAN)
+    table = np.repeat(c["table"], N, 0)
+    kv = gdn.PagedKV(kv.k, kv.v, torch.tensor(table, dtype=torch.int32).cuda(),
+                     torch.full((N,), lens, dtype=torch.int32, device="cuda"), kv.weights)
+    c["table"], c["lens"] = table, np.full(N, lens)
+    q, q64 = query(N, 2 * G, d, io, 18)
+    check(kv, c, q, q64, io, d ** -0.5, 0, True)
+
+
+def test_a_wide_table_needs_no_more_workspace_than_the_pool():
+    kv, _ = cache([100, 30], 16, 2, 64, "bf16", 19)
+    wide = torch.zeros(2, 1 << 16, dtype=torch.int32, device="cuda")
+    wide[:, :kv.block_table.shape[1]] = kv.block_table
+    big = gdn.PagedKV(kv.k, kv.v, wide, kv.seq_lens, kv.weights.clone())
+    assert gdn.gdn2_attn_decode_workspace_bytes(big, 8, True) < 32 << 20
+    q, _ = query(2, 8, 64, "bf16", 20)
+    a, b = (gdn.attn_decode_step(q, x, add_weights=True, want_lse=True) for x in (kv, big))
+    # the narrow table takes each head in one block, the wide one in parts
+    assert torch.allclose(a[0].float(), b[0].float(), rtol=2 ** -7, atol=2 ** -8)
+    assert torch.allclose(a[1], b[1], rtol=0, atol=1e-5)
+    assert torch.allclose(kv.weights, big.weights, rtol=1e-5, atol=1e-6)
+
+
 # ----------------------------------------------------------------------- append
 
 @pytest.mark.parametrize("io", ["bf16", "f32"])
@@ -327,6 +355,70 @@ def test_evict_very_long(length, budget):
     P = 64
     new = np.arange(budget)
     assert np.array_equal(h["k"][c["table"][0, new // P], new % P, 0], k0[c["table"][0, kept // P], kept % P, 0])
+
+
+@pytest.mark.parametrize("lens,budget,H_kv,page", [([20000, 19000, 1], 18990, 3, 16), ([9000] * 5, 4500, 4, 64),
+                                                   ([30000], 29999, 1, 7), ([3000] * 40, 100, 8, 32)])
+def test_evict_in_place_agrees_with_another_cache(lens, budget, H_kv, page):
+    """Many blocks shift rows at once, down to one row a token: what they read must not have
+    been written over."""
+    for seed in range(3):
+        kv, _ = cache_on_gpu(lens, page, H_kv, 128, 70 + seed)
+        dst, _ = cache_on_gpu([min(x, budget) for x in lens], page, H_kv, 128, 80 + seed)
+        a = gdn.kv_evict(kv, budget, sink=2, recent=3, dst=dst, want_kept=True)
+        b = gdn.kv_evict(kv, budget, sink=2, recent=3, want_kept=True)
+        assert gdn.gdn2_get_device_status() == 0
+        assert torch.equal(a, b) and torch.equal(kv.seq_lens, dst.seq_lens)
+        for n, x in enumerate(lens):
+            j = torch.arange(min(x, budget), device="cuda")
+            p, p2 = kv.block_table[n, j // page].long(), dst.block_table[n, j // page].long()
+            assert torch.equal(kv.k[p, j % page], dst.k[p2, j % page])
+            assert torch.equal(kv.v[p, j % page], dst.v[p2, j % page])
+            assert torch.equal(kv.weights[p, :, j % page], dst.weights[p2, :, j % page])
+
+
+def cache_on_gpu(lens, page, H_kv, d, seed):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    need = [-(-x // page) for x in lens]
+    perm = torch.randperm(sum(need), device="cuda", generator=g).to(torch.int32)
+    table = torch.full((len(lens), max(need)), -1, dtype=torch.int32, device="cuda")
+    at = 0
+    for n, y in enumerate(need):
+        table[n, :y] = perm[at:at + y]
+        at += y
+    k, v = (torch.randn(sum(need), page, H_kv, d, device="cuda", generator=g).to(torch.bfloat16) for _ in range(2))
+    w = torch.rand(sum(need), H_kv, page, device="cuda", generator=g)
+    return gdn.PagedKV(k, v, table, torch.tensor(lens, dtype=torch.int32, device="cuda"), w), None
+
+
+def test_evict_into_other_pages_of_the_same_pool():
+    """Two sequences that share their prompt's pages, evicted into pages of their own."""
+    kv, c = cache([64, 64, 0], 16, 2, 32, "f32", 49, room=32)
+    for t in (kv.block_table, c["table"]):
+        t[1, :4] = t[0, :4]
+    free = sorted(set(range(c["k"].shape[0])) - set(c["table"][:2, :4].ravel().tolist()))
+    dst_table = torch.tensor([free[:2], free[2:4], free[4:6]], dtype=torch.int32, device="cuda")
+    dst = gdn.PagedKV(kv.k, kv.v, dst_table, torch.zeros(3, dtype=torch.int32, device="cuda"), kv.weights)
+    c2 = dict(c, table=dst_table.cpu().numpy(), lens=np.zeros(3, dtype=np.int64))
+    weighted(kv, c, "random", 5)
+    ref = paged.evict(c, 20, 2, 3, c2)
+    kept = gdn.kv_evict(kv, 20, sink=2, recent=3, dst=dst, want_kept=True)
+    assert np.array_equal(kept.cpu().numpy(), ref)
+    h = host(dst)
+    assert all(same(h[x], c2[x]) for x in ("k", "v", "w", "lens"))
+
+
+def test_evict_with_a_budget_beyond_the_table():
+    kv, c = cache([50, 20], 16, 1, 32, "f32", 53)
+    dst, c2 = cache([50, 20], 16, 1, 32, "f32", 54)
+    before = host(kv)
+    assert torch.equal(gdn.kv_evict(kv, 70, want_kept=True)[1, 0, :22].cpu(), torch.tensor(list(range(20)) + [-1, -1], dtype=torch.int32))
+    h = host(kv)
+    assert all(same(h[x], before[x]) for x in ("k", "v", "w", "lens"))
+    paged.evict(c, 10 ** 5, 7, 9, c2)
+    gdn.kv_evict(kv, 10 ** 5, sink=7, recent=9, dst=dst)
+    h = host(dst)
+    assert all(same(h[x], c2[x]) for x in ("k", "v", "w", "lens"))
 
 
 @pytest.mark.parametrize("into", [False, True])

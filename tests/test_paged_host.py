@@ -80,7 +80,8 @@ def test_null_cache(L):
 @pytest.mark.parametrize("kw,status", [
     (dict(q=None), 1), (dict(o=None), 1), (dict(q=FAKE + 4), 1), (dict(o=FAKE + 8), 1), (dict(lse=FAKE + 2), 1),
     (dict(H=0), 1), (dict(H=6), 1), (dict(H=-4), 1), (dict(window=-1), 1),
-    (dict(scale=float("nan")), 1), (dict(scale=float("inf")), 1),
+    (dict(scale=float("nan")), 1), (dict(scale=float("inf")), 1), (dict(scale=3e38), 1), (dict(scale=-3e38), 1),
+    (dict(H=4 * 257), 2), (dict(kv=desc(N=1 << 20, max_pages=1 << 16)), 2),
     (dict(kv=desc(weight=None), add=1), 1),
     (dict(ws=None), 3), (dict(ws_bytes=0), 3), (dict(ws=FAKE + 8), 3),
     (dict(H=1 << 26), 2),
@@ -105,6 +106,7 @@ def test_append_refuses(L, kw, status):
     (dict(dst=desc(seq_lens=FAKE + 64, N=3)), 1), (dict(dst=desc(seq_lens=FAKE + 64, io=0)), 1),
     (dict(dst=desc(seq_lens=FAKE + 64, H_kv=2)), 1), (dict(dst=desc(seq_lens=FAKE + 64, d=32)), 1),
     (dict(ws=None), 3), (dict(ws_bytes=16), 3), (dict(ws=FAKE + 8), 3),
+    (dict(kv=desc(N=1 << 20, max_pages=1 << 20), budget=1 << 24), 2),
 ])
 def test_evict_refuses(L, kw, status):
     assert evict(L, **kw) == status
@@ -167,8 +169,11 @@ def test_binding_refuses_arguments(L):
         gdn.kv_append(kv, torch.zeros(3, 2, 32), torch.zeros(3, 2, 32), cu_seqlens=torch.zeros(4, dtype=torch.int64))
     with pytest.raises(ValueError, match="CUDA"):
         gdn.attn_decode_step(torch.zeros(3, 4, 32), kv)
-    with pytest.raises(ValueError, match="budget"):
-        gdn.kv_evict(kv, 0)
+    for kw in (dict(budget=0), dict(budget=2 ** 31), dict(budget=8, recent=2 ** 32), dict(budget=8, sink=-2 ** 33)):
+        with pytest.raises(ValueError):
+            gdn.kv_evict(kv, **kw)
+    with pytest.raises(ValueError, match="window"):
+        gdn.attn_decode_step(torch.zeros(3, 4, 32), kv, window=2 ** 32 + 4)
     with pytest.raises(ValueError):
         gdn.kv_append(kv, torch.zeros(3, 2, 32), torch.zeros(3, 2, 32), lens_out=torch.zeros(2, dtype=torch.int32))
 
