@@ -10,6 +10,10 @@
 // of at most 16 query heads), numbered in that order; every block takes an
 // equal run of consecutive units, whatever the sequences' lengths (the lengths
 // are on the device, so each block finds its own run with a scan over them).
+// Before each (sequence, head)'s units stand kLead empty ones, for the time
+// that starting and merging it takes: without them a block that gets 28 short
+// sequences needs twice as long as one with 28 units of a long one (64
+// sequences of 1 to 1000 tokens, 16 heads: 85 us without them, 51 with them).
 // A block walks the part of its run that lies in one (sequence, head) as a
 // segment with a running maximum m, sum l and accumulator of e^(s - m) v.  A
 // segment that covers the whole (sequence, head) leaves the result, one that
@@ -35,10 +39,15 @@ constexpr int kUnit = 64;        // tokens of a unit
 constexpr int kMostBlocksPerSm = 4;
 constexpr int kMostGroup = kMaxHeadGroup;
 constexpr int kHeadBlock = 16;   // most query heads of one pass
-constexpr int kMinUnits = 2;     // fewest units worth a block of their own
-// Tables that reach no further than this give each block one (sequence, head)
-// whole: no search for a run, no join.
-constexpr int kSoloTokens = 256;
+constexpr int kLead = 2;
+constexpr int kMinUnits = 1;     // fewest units worth a block of their own
+// Sequences that cannot hold more than kSoloTokens (or kSoloTokensMany where
+// there are kSoloRuns (sequence, head)s for each block that the GPU holds, so
+// that blocks with short ones make room for others) go to blocks one
+// (sequence, head) each: no search for a run, and no join.
+constexpr int kSoloTokens = 512;
+constexpr int kSoloTokensMany = 2048;
+constexpr int kSoloRuns = 3;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
@@ -63,7 +72,7 @@ struct AttnArgs {
 __device__ __forceinline__ int first_token(int len, int window) { return window > 0 && len > window ? len - window : 0; }
 __device__ __forceinline__ int units_of(const PagedView &c, int n, int window, unsigned int *status) {
     const int len = checked_len(c, n, status);
-    return (len - first_token(len, window) + kUnit - 1) / kUnit;
+    return len == 0 ? 0 : kLead + (len - first_token(len, window) + kUnit - 1) / kUnit;
 }
 
 // The run of units of block `block` out of `blocks`, `per` (= Hkv times
@@ -173,7 +182,7 @@ __device__ __forceinline__ bool next_segment(const AttnArgs &a, Run &run, Segmen
     const PagedView &c = a.c;
     const int per = c.Hkv * a.HB;
     while (run.u < run.end) {
-        const int len = checked_len(c, run.n, a.status), first = first_token(len, a.window);
+        const int n = run.n, len = checked_len(c, n, a.status), first = first_token(len, a.window);
         const int T = (len - first + kUnit - 1) / kUnit;
         int t0 = 0, cnt = T;
         if constexpr (SOLO) {
@@ -185,14 +194,21 @@ __device__ __forceinline__ bool next_segment(const AttnArgs &a, Run &run, Segmen
                 ++run.n;
                 continue;
             }
-            const int in = run.u - run.base;
-            sg.run = in / T;
-            t0 = in - sg.run * T;
-            cnt = min(T - t0, run.end - run.u);
-            sg.unit = run.u;
-            sg.run_end = run.base + (sg.run + 1) * T;
+            const int U = T + kLead, in = run.u - run.base;
+            sg.run = in / U;
+            const int u0 = in - sg.run * U, n_units = min(U - u0, run.end - run.u);
+            t0 = max(u0 - kLead, 0);
+            cnt = u0 + n_units - kLead - t0;  // without a leading unit's share: nothing to do if <= 0
+            sg.unit = run.u - u0 + kLead + t0;
+            sg.run_end = run.base + (sg.run + 1) * U;
+            run.u += n_units;
+            if (run.u == run.base + per * U) {
+                run.base = run.u;
+                ++run.n;
+            }
+            if (cnt <= 0) continue;
         }
-        sg.n = run.n;
+        sg.n = n;
         sg.h = sg.run / a.HB;
         const int hb = sg.run - sg.h * a.HB;
         sg.head = sg.h * a.G + hb * a.hpb;
@@ -201,13 +217,6 @@ __device__ __forceinline__ bool next_segment(const AttnArgs &a, Run &run, Segmen
         sg.end = min(len, sg.begin + cnt * kUnit);
         sg.starts = t0 == 0;
         sg.whole = t0 == 0 && cnt == T;
-        if constexpr (!SOLO) {
-            run.u += cnt;
-            if (run.u == run.base + per * T) {
-                run.base = run.u;
-                ++run.n;
-            }
-        }
         return true;
     }
     return false;
@@ -329,6 +338,7 @@ template <int D, int NT>
 struct EngineBf16 {
     using E = __nv_bfloat16;
     static constexpr int KW = 16, RB = 2 * D, kRows = 8 * NT, kBlocksPerSm = D == 128 ? 2 : 4, kStages = 3;
+    static constexpr int kSoloBlocksPerSm = D == 128 ? (NT == 1 ? 3 : 2) : D == 64 ? (NT == 1 ? 5 : 4) : 6, kSoloStages = 2;
     uint32_t qf[NT][D / 16][2];
     float acc[NT][D / 16][4];
     float m[NT][2], l[NT][2];
@@ -461,6 +471,7 @@ struct EngineF32 {
     static constexpr int KT = D == 128 || GP == 16 ? 1 : 2;
     static constexpr int KW = 8 * KT, RB = 4 * D, kRows = GP, kStages = 3;
     static constexpr int kBlocksPerSm = D == 32 && GP <= 4 ? 4 : 2;
+    static constexpr int kSoloBlocksPerSm = GP == 16 ? 2 : GP == 8 || D == 128 ? 3 : 4, kSoloStages = 2;
     static constexpr int kLanes = D / 4;         // lanes of one token's channels
     static constexpr int kGroups = 32 / kLanes;  // tokens at once
     static constexpr int kVec = GP < 4 ? GP : 4;  // heads whose weights lie together, and that
@@ -648,19 +659,19 @@ __device__ __forceinline__ void write_result(const AttnArgs &a, E *o, size_t hd,
 }
 
 // shared memory of a block: the warps' rings, then what the engine keeps
-template <class En, int D> constexpr int attn_smem() {
-    return kAttnWarps * Ring<En::KW, En::RB, En::kStages, false>::kBytes +
+template <class En, int D, bool SOLO> constexpr int attn_smem() {
+    return kAttnWarps * Ring<En::KW, En::RB, SOLO ? En::kSoloStages : En::kStages, SOLO>::kBytes +
            (sizeof(typename En::E) == 4 ? En::kRows * (D + kAttnWarps * En::KW) * 4 : 0);
 }
 
 // SOLO: block b takes run b whole (no parts, no join).
 template <class En, int D, bool SOLO>
-__global__ void __launch_bounds__(kAttnThreads, En::kBlocksPerSm)
+__global__ void __launch_bounds__(kAttnThreads, SOLO ? En::kSoloBlocksPerSm : En::kBlocksPerSm)
 attn_split_kernel(const AttnArgs a) {
     extern __shared__ __align__(128) unsigned char smem[];
     __shared__ float2 s_ml[kAttnWarps][En::kRows];
-    using R = Ring<En::KW, En::RB, En::kStages, SOLO>;
-    constexpr int kStages = En::kStages;
+    constexpr int kStages = SOLO ? En::kSoloStages : En::kStages;
+    using R = Ring<En::KW, En::RB, kStages, SOLO>;
     using E = typename En::E;
     static_assert(R::kStage >= En::kRows * D * 4, "a stage holds a warp's accumulator");
     float *own = reinterpret_cast<float *>(smem + kAttnWarps * R::kBytes);
@@ -849,14 +860,21 @@ __device__ __forceinline__ void add_weights(const AttnArgs &a, int first_block) 
             ++run.n;
             continue;
         }
-        const int h = (run.u - run.base) / T, t0 = run.u - run.base - h * T;
-        const int cnt = min(T - t0, run.end - run.u);
+        const int U = T + kLead, h = (run.u - run.base) / U, u0 = run.u - run.base - h * U;
+        const int n_units = min(U - u0, run.end - run.u), n = run.n, base = run.base;
+        const int t0 = max(u0 - kLead, 0), cnt = u0 + n_units - kLead - t0;
+        run.u += n_units;
+        if (run.u == run.base + c.Hkv * U) {
+            run.base = run.u;
+            ++run.n;
+        }
+        if (cnt <= 0) continue;
         __syncthreads();  // the last segment's s_L has been read
         for (int g = tid >> 5; g < a.G; g += NT / 32) {
             const int hb = g / a.hpb, row = g - hb * a.hpb;
-            const int2 pr = SOLO ? make_int2(-1, -1) : a.parts[((size_t)run.n * c.Hkv + h) * a.HB + hb];
+            const int2 pr = SOLO ? make_int2(-1, -1) : a.parts[((size_t)n * c.Hkv + h) * a.HB + hb];
             float L;
-            if (pr.x < 0) L = a.lse2[(size_t)run.n * a.H + h * a.G + g];
+            if (pr.x < 0) L = a.lse2[(size_t)n * a.H + h * a.G + g];
             else {
                 float m = -INFINITY, l = 0.f;
                 for (int b = pr.x + lane; b <= pr.y; b += 32) m = fmaxf(m, a.ml[part_row(pr, b, row)].x);
@@ -887,13 +905,13 @@ __device__ __forceinline__ void add_weights(const AttnArgs &a, int first_block) 
                 at[u] = u * kStep * a.hpb * kUnit;
                 int entry;
                 page_slot(c, j, entry, slot[u]);
-                page[u] = page_of(c, run.n, entry);
+                page[u] = page_of(c, n, entry);
             }
             for (int hb = 0; hb < a.HB; ++hb) {
                 // the split kernel's number of this unit: it has Hkv HB runs a sequence
                 const int run_of = h * a.HB + hb;
-                const int unit = SOLO ? (run.n * c.Hkv * a.HB + run_of) * ((c.cap + kUnit - 1) / kUnit) + t
-                                      : run.base * a.HB + run_of * T + t;
+                const int unit = SOLO ? (n * c.Hkv * a.HB + run_of) * ((c.cap + kUnit - 1) / kUnit) + t
+                                      : base * a.HB + run_of * U + kLead + t;
                 const float *s = a.scores + (size_t)unit * a.hpb * kUnit + tok;
                 const int rows = min(a.hpb, a.G - hb * a.hpb);
                 if (unit - t + min(t + (kAhead - 1) * kStep, t0 + cnt - 1) >= a.score_units) {
@@ -902,7 +920,7 @@ __device__ __forceinline__ void add_weights(const AttnArgs &a, int first_block) 
 #pragma unroll 1
                     for (int u = 0; u < kAhead; ++u)
                         if (page[u] >= 0)
-                            sum[u] += weight_of_row<E, D>(a, static_cast<const E *>(a.q) + ((size_t)run.n * a.H + h * a.G + hb * a.hpb) * D,
+                            sum[u] += weight_of_row<E, D>(a, static_cast<const E *>(a.q) + ((size_t)n * a.H + h * a.G + hb * a.hpb) * D,
                                                           reinterpret_cast<const E *>(c.k + row_off(c, page[u], slot[u], h)),
                                                           s_L + hb * a.hpb, rows);
                     continue;
@@ -921,11 +939,6 @@ __device__ __forceinline__ void add_weights(const AttnArgs &a, int first_block) 
             for (int u = 0; u < kAhead; ++u)
                 if (page[u] >= 0) atomicAdd(c.w + weight_off(c, page[u], slot[u], h), sum[u]);
         }
-        run.u += cnt;
-        if (run.u == run.base + c.Hkv * T) {
-            run.base = run.u;
-            ++run.n;
-        }
     }
 }
 
@@ -940,19 +953,30 @@ attn_finish_kernel(const AttnArgs a) {
 
 // ---- host side
 static void head_blocks(const PagedView &c, int H, AttnArgs &a) {
+    a.c = c;
     a.H = H;
     a.G = H / c.Hkv;
     a.HB = (a.G + kHeadBlock - 1) / kHeadBlock;
     a.hpb = (a.G + a.HB - 1) / a.HB;
 }
 
+// The kept scores of a solo call are laid out by what the table reaches, so the
+// window counts only without them (the workspace query does not know it).
+static bool solo(const AttnArgs &a, bool weights, int window) {
+    const PagedView &c = a.c;
+    const int reach = window > 0 && !weights ? min(window, c.cap) : c.cap;
+    return reach <= kSoloTokens || (reach <= kSoloTokensMany && (long long)c.N * c.Hkv * a.HB >= kSoloRuns * 2LL * sm_count());
+}
+static bool solo(const AttnArgs &a) { return solo(a, a.scores != nullptr, a.window); }
+
 // places the workspace's regions (ws may be null: sizes only); returns its bytes
-static size_t attn_ws(const PagedView &c, AttnArgs &a, int add_weights, void *ws) {
+static size_t attn_ws(AttnArgs &a, int add_weights, void *ws) {
+    const PagedView &c = a.c;
     a.ml = nullptr;
     a.part = a.lse2 = a.scores = nullptr;
     a.score_units = 0;
     a.parts = nullptr;
-    if (c.cap <= kSoloTokens && !add_weights) return 256;  // not touched
+    if (!add_weights && solo(a, false, 0)) return 256;  // not touched
     const size_t slots = 2 * (size_t)kMostBlocksPerSm * sm_count(), runs = (size_t)c.N * c.Hkv * a.HB;
     size_t o = 0;
     auto take = [&](size_t bytes) { const size_t at = o; o = align256(o + bytes); return static_cast<char *>(ws) + at; };
@@ -963,9 +987,9 @@ static size_t attn_ws(const PagedView &c, AttnArgs &a, int add_weights, void *ws
         a.lse2 = reinterpret_cast<float *>(take((size_t)c.N * a.H * sizeof(float)));
         // every unit there can be, or if that is less, as many as the pool has
         // tokens for; a table much wider than the sequences costs nothing
-        const long long all = (long long)runs * ((c.cap + kUnit - 1) / kUnit);
-        const long long pool = ((long long)c.num_pages * c.page / kUnit + c.N) * c.Hkv * a.HB;
-        a.score_units = (int)(c.cap <= kSoloTokens || all < pool ? all : pool);
+        const long long all = (long long)runs * ((c.cap + kUnit - 1) / kUnit + kLead);
+        const long long pool = ((long long)c.num_pages * c.page / kUnit + (1 + kLead) * (long long)c.N) * c.Hkv * a.HB;
+        a.score_units = (int)(solo(a, true, 0) || all < pool ? all : pool);
         a.scores = reinterpret_cast<float *>(take((size_t)a.score_units * a.hpb * kUnit * sizeof(float)));
     }
     return o;
@@ -975,19 +999,19 @@ static size_t attn_ws(const PagedView &c, AttnArgs &a, int add_weights, void *ws
 bool attn_countable(const PagedView &c, int H) {
     AttnArgs a;
     head_blocks(c, H, a);
-    return (double)c.N * c.Hkv * a.HB * ((c.cap + kUnit - 1) / kUnit) < (double)(1 << 30);
+    return (double)c.N * c.Hkv * a.HB * ((c.cap + kUnit - 1) / kUnit + kLead) < (double)(1 << 30);
 }
 
 size_t attn_ws_bytes(const PagedView &c, int H, int add_weights) {
     AttnArgs a;
     head_blocks(c, H, a);
-    return attn_ws(c, a, add_weights, nullptr);
+    return attn_ws(a, add_weights, nullptr);
 }
 
 template <class En, int D, bool SOLO>
 static cudaError_t attn_run_as(const AttnArgs &a, cudaStream_t s) {
     static_assert(En::kBlocksPerSm <= kMostBlocksPerSm, "the workspace has parts for so many");
-    constexpr int bytes = attn_smem<En, D>();
+    constexpr int bytes = attn_smem<En, D, SOLO>();
     using E = typename En::E;
     const int heads = a.c.N * a.H;
     cudaError_t e = cudaFuncSetAttribute(attn_split_kernel<En, D, SOLO>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
@@ -1004,7 +1028,7 @@ static cudaError_t attn_run_as(const AttnArgs &a, cudaStream_t s) {
 }
 template <class En, int D>
 static cudaError_t attn_run(const AttnArgs &a, cudaStream_t s) {
-    return a.c.cap <= kSoloTokens ? attn_run_as<En, D, true>(a, s) : attn_run_as<En, D, false>(a, s);
+    return solo(a) ? attn_run_as<En, D, true>(a, s) : attn_run_as<En, D, false>(a, s);
 }
 
 template <int D>
@@ -1020,7 +1044,6 @@ static cudaError_t attn_for_d(const AttnArgs &a, cudaStream_t s) {
 cudaError_t attn_launch(const PagedView &c, const void *q, void *o, float *lse, int H, float scale, int window,
                         int add_weights, void *ws, unsigned int *status, cudaStream_t s) {
     AttnArgs a;
-    a.c = c;
     a.q = q;
     a.o = o;
     a.lse = lse;
@@ -1028,7 +1051,7 @@ cudaError_t attn_launch(const PagedView &c, const void *q, void *o, float *lse, 
     a.scale2 = scale * kLog2e;
     a.window = window;
     a.status = status;
-    attn_ws(c, a, add_weights, ws);
+    attn_ws(a, add_weights, ws);
     if (c.d == 32) return attn_for_d<32>(a, s);
     if (c.d == 64) return attn_for_d<64>(a, s);
     return attn_for_d<128>(a, s);
