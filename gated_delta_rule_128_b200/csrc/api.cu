@@ -571,7 +571,7 @@ const char *gdn2_status_string(gdn2_status status) {
     switch (status) {
         case GDN2_OK: return "ok";
         case GDN2_ERR_INVALID_ARG: return "invalid argument (null or misaligned pointer, bad size)";
-        case GDN2_ERR_UNSUPPORTED: return "unsupported size (d_k, d_v in {32,64,128}; chunk in {16,32,64})";
+        case GDN2_ERR_UNSUPPORTED: return "unsupported size (d_k, d_v, d in {32,64,128}; chunk in {16,32,64}; see gdn2.h)";
         case GDN2_ERR_WORKSPACE: return "workspace missing, misaligned or too small";
         case GDN2_ERR_CUDA: return "CUDA error";
         case GDN2_ERR_TIMEOUT: return "a kernel gave up on a bounded wait";
@@ -580,7 +580,7 @@ const char *gdn2_status_string(gdn2_status status) {
     return "unknown status";
 }
 
-int gdn2_version(void) { return 200; }
+int gdn2_version(void) { return 300; }
 
 unsigned long long gdn2_kernel_launches(void) { return g_launches.load(); }
 

@@ -20,7 +20,7 @@ gdn2_status make_view(PagedView &c, const gdn2_paged_kv *kv) {
     if (kv->num_pages < 1 || kv->page_size < 1 || kv->max_pages < 1 || kv->N < 1 || kv->H_kv < 1)
         return GDN2_ERR_INVALID_ARG;
     if (kv->d != 32 && kv->d != 64 && kv->d != 128) return GDN2_ERR_UNSUPPORTED;
-    if ((long long)kv->max_pages * kv->page_size > 0x7fffffffLL - 1024) return GDN2_ERR_UNSUPPORTED;
+    if ((long long)kv->max_pages * kv->page_size > 1LL << 30) return GDN2_ERR_UNSUPPORTED;  // token numbers are ints
     // one block per (sequence, head) in the calls that split no further
     if ((long long)kv->N * kv->H_kv > 0x7fffffffLL / 64) return GDN2_ERR_UNSUPPORTED;
     const int es = kv->io == GDN2_IO_BF16 ? 2 : 4;

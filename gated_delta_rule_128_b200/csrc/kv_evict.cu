@@ -243,8 +243,10 @@ evict_select_kernel(const PagedView c, const PagedView to, int in_place, int bud
         const unsigned eq = __ballot_sync(0xffffffffu, j < wb && k == prefix);
         if (j < wb) {
             const int e = cnt.y + __popc(eq & below);
-            if (k > prefix || (k == prefix && e < need)) list[sink + cnt.x + __popc(gt & below) + min(e, need)] = j;
-            else first = min(first, j);
+            if (k > prefix || (k == prefix && e < need)) {
+                const int at = sink + cnt.x + __popc(gt & below) + min(e, need);
+                if (at < sink + T) list[at] = j;  // always, unless the weights change under the call
+            } else first = min(first, j);
         }
         cnt.x += __popc(gt);
         cnt.y += __popc(eq);

@@ -74,7 +74,7 @@ typedef struct CUstream_st *gdn2_stream_t;
 typedef enum {
     GDN2_OK = 0,
     GDN2_ERR_INVALID_ARG = 1,  /* null pointer, bad size, misaligned pointer   */
-    GDN2_ERR_UNSUPPORTED = 2,  /* d_k, d_v or chunk outside the supported set  */
+    GDN2_ERR_UNSUPPORTED = 2,  /* d_k, d_v, chunk or another size outside the supported set */
     GDN2_ERR_WORKSPACE = 3,    /* workspace missing or smaller than required   */
     GDN2_ERR_CUDA = 4,         /* a CUDA launch or runtime call failed          */
     GDN2_ERR_TIMEOUT = 5,      /* a kernel gave up on a bounded wait            */
@@ -249,13 +249,14 @@ gdn2_status gdn2_bwd_varlen(const void *q, const void *k, const void *v, const v
  *   block_table : device int32 [N, max_pages]; entries behind a sequence's
  *       last page are not read.  seq_lens : device int32 [N].
  *   Supported: d in {32, 64, 128}; page_size, max_pages, num_pages, N >= 1;
- *       max_pages * page_size <= 2^31 - 1 - 1024.  N sequences may be empty.
+ *       max_pages * page_size <= 2^30; N * H_kv < 2^25.  Sequences may be empty.
  * k and v are 16-byte aligned; weight, block_table and seq_lens 4-byte.
  * Both tables are read on the device only.  A length outside 0 .. max_pages *
  * page_size makes the call treat that sequence as empty (and write none of
  * it), a block_table entry that is needed but outside 0 .. num_pages - 1 makes
  * it leave that page's tokens out; either records GDN2_ERR_INVALID_ARG in the
- * device status word.  No access leaves the pools.
+ * device status word.  No access leaves the pools.  Neither table, nor the
+ * weights, may change while a call that reads them runs.
  * Sequences may share pages (a common prompt) in every call that only reads
  * them; a page that a call writes must belong to one sequence, once. */
 typedef struct {

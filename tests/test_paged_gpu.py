@@ -220,6 +220,28 @@ def test_a_wide_table_needs_no_more_workspace_than_the_pool():
     assert torch.allclose(kv.weights, big.weights, rtol=1e-5, atol=1e-6)
 
 
+def test_attention_takes_the_callers_buffers():
+    kv, _ = cache([2000, 3], 16, 2, 64, "bf16", 22)
+    q, _ = query(2, 8, 64, "bf16", 23)
+    n = kv.workspace_bytes("gdn2_attn_decode_workspace_bytes", 8, False)
+    ws, o = torch.empty(n, dtype=torch.uint8, device="cuda"), torch.full_like(q, NAN)
+    a = gdn.attn_decode_step(q, kv)[0]
+    b, lse = gdn.attn_decode_step(q, kv, o=o, ws=ws)
+    assert b is o and lse is None and torch.equal(a, b)
+    with pytest.raises(gdn.Gdn2Error) as e:
+        gdn.attn_decode_step(q, kv, ws=ws[:n - 256])
+    assert e.value.status == 3
+    with pytest.raises(ValueError):
+        gdn.attn_decode_step(q, kv, o=torch.empty(2, 8, 32, dtype=torch.bfloat16, device="cuda"))
+    with pytest.raises(ValueError):
+        gdn.attn_decode_step(q, kv, ws=torch.empty(n, dtype=torch.uint8))
+    with pytest.raises(ValueError):
+        gdn.attn_decode_step(q.cpu(), kv)
+    with pytest.raises(gdn.Gdn2Error) as e:
+        gdn.attn_decode_step(q, gdn.PagedKV(kv.k, kv.v, kv.block_table, kv.seq_lens), add_weights=True)
+    assert e.value.status == 1
+
+
 # ----------------------------------------------------------------------- append
 
 @pytest.mark.parametrize("io", ["bf16", "f32"])

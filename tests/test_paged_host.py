@@ -48,6 +48,7 @@ BAD_CACHES = [
     (dict(io=2), 1), (dict(N=0), 1), (dict(H_kv=0), 1), (dict(num_pages=0), 1), (dict(page_size=-1), 1),
     (dict(max_pages=0), 1), (dict(d=48), 2), (dict(d=256), 2),
     (dict(max_pages=1 << 20, page_size=1 << 11, stride_page=1 << 20), 2),
+    (dict(max_pages=(1 << 26) + 1), 2),
     (dict(N=1 << 25, H_kv=4), 2),
     (dict(stride_head=60), 1),          # rows overlap
     (dict(stride_head=65), 1),          # not 16 bytes
