@@ -155,6 +155,9 @@ __device__ __forceinline__ void ldmatrix4_trans(uint32_t addr, uint32_t *r) {
     asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
                  : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
 }
+// the two values of a packed pair of bf16
+__device__ __forceinline__ float bf16_low(uint32_t x) { return __uint_as_float(x << 16); }
+__device__ __forceinline__ float bf16_high(uint32_t x) { return __uint_as_float(x & 0xffff0000u); }
 // an 8 x 8 block of 16-bit values (thread 4 r + c holds row r, columns 2c, 2c + 1), transposed
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
     uint32_t y;
@@ -417,7 +420,7 @@ struct EngineBf16 {
                     }
                 }
         }
-        uint32_t p[NT][2];
+        uint32_t p[NT][2], rest[NT][2];
 #pragma unroll
         for (int i = 0; i < NT; ++i) {
 #pragma unroll
@@ -427,17 +430,27 @@ struct EngineBf16 {
                 s[i][2 + y] = exp2f(s[i][2 + y] - ref);
                 l[i][y] += s[i][y] + s[i][2 + y];
             }
-            // the only rounding on the way: weights in [0, 1] to bf16, the type of
-            // the v that they multiply; the sum takes them unrounded
-            p[i][0] = transpose8x8(tc::pack_bf16(s[i][0], s[i][1]));
-            p[i][1] = transpose8x8(tc::pack_bf16(s[i][2], s[i][3]));
+            // The weights meet v as the sum of two bf16 numbers: rounded once,
+            // to 2^-8, they would add as much error to o as its own rounding
+            // (2.2e-3 against 1.7e-3 in all); in two parts it is 2^-16.  The
+            // second product costs nothing up to 8 heads, where the copies set
+            // the pace, and 5% with 16 (64 sequences of up to 4000 tokens, 4 kv
+            // heads: 62.7 -> 65.8 us).
+            const uint32_t h0 = tc::pack_bf16(s[i][0], s[i][1]), h1 = tc::pack_bf16(s[i][2], s[i][3]);
+            p[i][0] = transpose8x8(h0);
+            p[i][1] = transpose8x8(h1);
+            rest[i][0] = transpose8x8(tc::pack_bf16(s[i][0] - bf16_low(h0), s[i][1] - bf16_high(h0)));
+            rest[i][1] = transpose8x8(tc::pack_bf16(s[i][2] - bf16_low(h1), s[i][3] - bf16_high(h1)));
         }
 #pragma unroll
         for (int x = 0; x < D / 16; ++x) {
             uint32_t v[4];
             ldmatrix4_trans(vs + R::at((mi >> 1) * 8 + lr, 2 * x + (mi & 1)), v);
 #pragma unroll
-            for (int i = 0; i < NT; ++i) mma16816(acc[i][x], v, p[i][0], p[i][1]);
+            for (int i = 0; i < NT; ++i) {
+                mma16816(acc[i][x], v, p[i][0], p[i][1]);
+                mma16816(acc[i][x], v, rest[i][0], rest[i][1]);
+            }
         }
     }
     // this warp's m, l [kRows] and acc [kRows][D] to shared memory

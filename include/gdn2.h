@@ -304,8 +304,8 @@ size_t gdn2_attn_decode_workspace_bytes(const gdn2_paged_kv *kv, int H, int add_
  *       share a page, each adds to it, in no fixed order.
  *   scale : finite.  The cache is only read.
  * bf16: products on the tensor cores, float32 scores and sums; the softmax
- * weights are rounded to bf16 for the product with v.  float32: all of it in
- * float32. */
+ * weights meet v as sums of two bf16 numbers (off by 2^-16 at most).  float32:
+ * all of it in float32. */
 gdn2_status gdn2_attn_decode_step(const gdn2_paged_kv *kv, const void *q, void *o, float *lse,
                                   int H, float scale, int window, int add_weights, void *ws,
                                   size_t ws_bytes, gdn2_stream_t stream);

@@ -70,11 +70,12 @@ def bounds(io, o, lse, a, smax, length, d):
     A softmax weight before normalisation, e^(s - m): m is one of the computed scores, so the
     exponent is off by 2 ds, and e^x itself by 2^-21 (exp2 and the subtraction's rounding are
     relative to the exponent, again within ds).  Sums over the tokens: `length` 2^-24, twice
-    (numerator and denominator), and the rescalings and joins 64 2^-24.  bf16 rounds each
-    weight before the product with v (2^-8 of sum p |v| = a) and the result (2^-8 |o|)."""
+    (numerator and denominator), and the rescalings and joins 64 2^-24.  bf16 takes
+    each weight in two parts, the second rounded (2^-8 of the at most 2^-8 that the first
+    leaves), and rounds the result (2^-8 |o|)."""
     ds = (2 * d * 2.0 ** -24 + 2.0 ** -22) * smax
     p = 4 * ds + 2 * 2.0 ** -21 + (2 * length + 64) * 2.0 ** -24
     half = 2.0 ** -8 if io == "bf16" else 2.0 ** -24
-    b = (p[..., None] + (2.0 ** -8 if io == "bf16" else 0.0)) * a * (1 + 2.0 ** -7) + half * np.abs(o) * (1 + 2.0 ** -7)
+    b = (p[..., None] + (2.0 ** -16 if io == "bf16" else 0.0)) * a * (1 + 2.0 ** -7) + half * np.abs(o) * (1 + 2.0 ** -7)
     fin = np.where(np.isfinite(lse), np.abs(lse), 0.0)
     return b + 1e-30, 2 * ds + 2.0 ** -21 + (length + 64) * 2.0 ** -24 + 2.0 ** -23 * (1 + fin), p

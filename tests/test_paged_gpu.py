@@ -143,7 +143,8 @@ def test_attention_infinite_scores(io):
     o, lse = gdn.attn_decode_step(q.cuda(), kv, scale=0.1, add_weights=True, want_lse=True)
     assert (o[1] == 0).all() and torch.isneginf(lse[1]).all()
     got = o.double().cpu().numpy()
-    assert (np.abs(got - r) <= (2.0 ** -7 if io == "bf16" else 1e-5) * (a + np.abs(r)) + 1e-30).all()
+    # rounding o, and 1e-4 of sum p |v| for scores of at most sum |q k| / 10 < 20
+    assert (np.abs(got - r) <= (2.0 ** -8 if io == "bf16" else 0) * np.abs(r) * 1.01 + 1e-4 * a + 1e-30).all()
     assert torch.isfinite(kv.weights).all()
 
 
