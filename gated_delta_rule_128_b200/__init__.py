@@ -468,7 +468,8 @@ class PagedKV:
     contents may change at any time (the table and lengths are read by the
     kernels); a cache of other tensors is another object."""
 
-    __slots__ = ("k", "v", "block_table", "seq_lens", "weights", "device", "struct", "ref", "_ws_bytes", "_untouched")
+    __slots__ = ("k", "v", "block_table", "seq_lens", "weights", "device", "index", "struct", "ref", "_ws_bytes",
+                 "_untouched")
 
     def __init__(self, k, v, block_table, seq_lens, weights=None):
         if k.dim() != 4 or v.shape != k.shape:
@@ -494,6 +495,7 @@ class PagedKV:
             _tensor("weights", weights, torch.float32, (pages, H, page), k.device)
         self.k, self.v, self.block_table, self.seq_lens, self.weights = k, v, block_table, seq_lens, weights
         self.device = k.device
+        self.index = k.device.index if k.is_cuda else -1  # the CUDA device
         self.struct = _PagedKVStruct(k.data_ptr(), v.data_ptr(),
                                      weights.data_ptr() if weights is not None else None,
                                      block_table.data_ptr(), seq_lens.data_ptr(), *strides, pages, page, width,
@@ -535,11 +537,9 @@ def _on_stream(kv: PagedKV, stream):
         if stream.device != kv.device:
             raise ValueError(f"the stream is on {stream.device}, the cache on {kv.device}")
         return torch.cuda.stream(stream)
-    if kv.device.type != "cuda":
+    if kv.index < 0:
         raise ValueError(f"the cache is on {kv.device}: its calls need a CUDA device")
-    if torch.cuda.current_device() != kv.device.index:
-        return torch.cuda.device(kv.device)
-    return _HERE
+    return _HERE if torch._C._cuda_getDevice() == kv.index else torch.cuda.device(kv.device)
 
 
 def kv_append(kv: PagedKV, k, v, *, cu_seqlens=None, lens_out=None, stream=None) -> None:
@@ -561,7 +561,7 @@ def kv_append(kv: PagedKV, k, v, *, cu_seqlens=None, lens_out=None, stream=None)
     with _on_stream(kv, stream):
         rc = lib().gdn2_kv_append(kv.ref, k.data_ptr(), v.data_ptr(),
                                   None if cu_seqlens is None else cu_seqlens.data_ptr(), T,
-                                  lens_out.data_ptr(), _raw_stream(kv.device.index))
+                                  lens_out.data_ptr(), _raw_stream(kv.index))
     if rc:
         raise Gdn2Error("gdn2_kv_append", rc)
 
@@ -592,7 +592,7 @@ def attn_decode_step(q, kv: PagedKV, *, scale: Optional[float] = None, window: i
         ws = kv._workspace(ws, "gdn2_attn_decode_workspace_bytes", H, bool(add_weights))
         rc = lib().gdn2_attn_decode_step(kv.ref, q.data_ptr(), o.data_ptr(), None if lse is None else lse.data_ptr(),
                                          H, s.d ** -0.5 if scale is None else scale, window, bool(add_weights),
-                                         ws.data_ptr(), ws.nbytes, _raw_stream(kv.device.index))
+                                         ws.data_ptr(), ws.nbytes, _raw_stream(kv.index))
     if rc:
         raise Gdn2Error("gdn2_attn_decode_step", rc)
     return o, lse
@@ -611,11 +611,11 @@ def kv_evict(kv: PagedKV, budget: int, *, sink: int = 0, recent: int = 0, dst: O
     if not (1 <= budget < 2 ** 31 and 0 <= sink <= budget and 0 <= recent <= budget - sink):
         raise ValueError(f"budget must be at least 1 and sink + recent within it, got {budget}, {sink}, {recent}")
     with _on_stream(kv, stream):
-        kept = torch.empty((s.N, s.H_kv, budget), dtype=torch.int32, device=kv.device) if want_kept else None
+        kept = torch.empty(s.N, s.H_kv, budget, dtype=torch.int32, device=kv.device) if want_kept else None
         ws = kv._workspace(ws, "gdn2_kv_evict_workspace_bytes", budget)
         rc = lib().gdn2_kv_evict(kv.ref, None if dst is None else dst.ref, budget, sink, recent,
                                  None if kept is None else kept.data_ptr(), ws.data_ptr(), ws.nbytes,
-                                 _raw_stream(kv.device.index))
+                                 _raw_stream(kv.index))
     if rc:
         raise Gdn2Error("gdn2_kv_evict", rc)
     return kept
