@@ -266,7 +266,7 @@ evict_select_kernel(const PagedView c, const PagedView to, int in_place, int bud
 // of one (sequence, head), a thread carrying the same 16-byte piece of kDeep
 // rows of k and of v; the next item's places are looked up (list, then tables)
 // while this one's rows are on their way.  The weights are items of their own.
-constexpr int kDeep = 2;
+constexpr int kDeep = 2;  // 16 sequences to 2K tokens of 16 heads: 113 us; with 4 rows a thread 121 to 127, with 8 149
 constexpr int kCopyBlocksPerSm = 4;
 
 // The most rows that any of the lists moves, for every thread of the block:
@@ -374,6 +374,8 @@ evict_copy_kernel(const PagedView c, const PagedView to, int stride, const int *
     }
 }
 
+constexpr int kShiftDeep = 8;
+constexpr int kShiftBlocksPerSm = 2;
 // In place, where a row may overwrite one that is still to be read.  Chunks of
 // rows are taken in the order of a ticket: chunk by chunk, in each the
 // (sequence, head)s.  A block reads its chunk, says so in the chunk's flag, and
@@ -382,8 +384,10 @@ evict_copy_kernel(const PagedView c, const PagedView to, int stride, const int *
 // chunks up to x.  No block waits before it has read its own chunk, and it
 // waits for blocks with earlier tickets only, which are at work already, so
 // every wait ends whichever blocks the GPU runs; it gives up all the same
-// after some seconds (GDN2_ERR_TIMEOUT).
-__global__ void __launch_bounds__(kMoveThreads, kCopyBlocksPerSm)
+// after some seconds (GDN2_ERR_TIMEOUT).  Chunks of 128 rows (bf16, d = 128)
+// make the agreement cheap: 16 sequences of up to 8K tokens and 16 heads to 2K
+// take 140 us, with 32 rows and twice the blocks 153; the copy above, 113.
+__global__ void __launch_bounds__(kMoveThreads, kShiftBlocksPerSm)
 evict_shift_kernel(const PagedView c, int stride, int chunks, const int *list_all, const EvictPlan *plan, int *flags,
                    int *ticket, unsigned int *status) {
     __shared__ int s_ticket;
@@ -391,30 +395,32 @@ evict_shift_kernel(const PagedView c, int stride, int chunks, const int *list_al
     const int piece = threadIdx.x % pieces, r = threadIdx.x / pieces;
     follow_previous();
     write_lens(c, plan);
-    const long long total = (long long)nhs * ((most_rows(plan, nhs) + at_once * kDeep - 1) / (at_once * kDeep));
+    const long long total = (long long)nhs * ((most_rows(plan, nhs) + at_once * kShiftDeep - 1) / (at_once * kShiftDeep));
     if (total == 0) return;
+    int next = threadIdx.x == 0 ? atomicAdd(ticket, 1) : 0;
     for (;;) {
         __syncthreads();  // the last ticket has been read
-        if (threadIdx.x == 0) s_ticket = atomicAdd(ticket, 1);
+        if (threadIdx.x == 0) s_ticket = next;
         __syncthreads();
         const long long x = (unsigned)s_ticket;
+        if (threadIdx.x == 0 && x < total) next = atomicAdd(ticket, 1);  // under this chunk's reads
         if (x >= total) return;
         const int chunk = (int)(x / nhs), nh = (int)(x - (long long)chunk * nhs), n = nh / c.Hkv, h = nh - n * c.Hkv;
         const EvictPlan p = plan[nh];
-        const long long i0 = p.first + (long long)chunk * at_once * kDeep;
+        const long long i0 = p.first + (long long)chunk * at_once * kShiftDeep;
         if (i0 >= p.count) continue;
         const int *list = list_all + (size_t)nh * stride;
         int *flag = flags + (size_t)nh * chunks;
-        uint4 k[kDeep], v[kDeep];
-        float w[kDeep];
-        int src[kDeep], page[kDeep], slot[kDeep];
+        uint4 k[kShiftDeep], v[kShiftDeep];
+        float w[kShiftDeep];
+        int src[kShiftDeep], page[kShiftDeep], slot[kShiftDeep];
 #pragma unroll
-        for (int u = 0; u < kDeep; ++u) {
+        for (int u = 0; u < kShiftDeep; ++u) {
             const long long i = i0 + r + u * at_once;
             src[u] = i < p.count ? list[i] : -1;
         }
 #pragma unroll
-        for (int u = 0; u < kDeep; ++u) {
+        for (int u = 0; u < kShiftDeep; ++u) {
             page[u] = -1;
             if (src[u] < 0) continue;
             int entry;
@@ -423,7 +429,7 @@ evict_shift_kernel(const PagedView c, int stride, int chunks, const int *list_al
             if (page[u] < 0) record_status(status, GDN2_ERR_INVALID_ARG);
         }
 #pragma unroll
-        for (int u = 0; u < kDeep; ++u) {
+        for (int u = 0; u < kShiftDeep; ++u) {
             if (page[u] < 0) continue;
             const long long at = row_off(c, page[u], slot[u], h) + piece * 16;
             k[u] = *reinterpret_cast<const uint4 *>(c.k + at);
@@ -446,7 +452,7 @@ evict_shift_kernel(const PagedView c, int stride, int chunks, const int *list_al
             continue;
         }
 #pragma unroll
-        for (int u = 0; u < kDeep; ++u) {
+        for (int u = 0; u < kShiftDeep; ++u) {
             if (page[u] < 0) continue;
             int entry, to_slot;
             page_slot(c, (int)(i0 + r + u * at_once), entry, to_slot);
@@ -466,9 +472,12 @@ evict_shift_kernel(const PagedView c, int stride, int chunks, const int *list_al
 // entries of a list in the workspace
 static int list_stride(const PagedView &c, int budget) { return budget < c.cap ? budget : c.cap; }
 
-// rows of a chunk, and chunks of a list
-static int chunk_rows(const PagedView &c) { return kMoveThreads / (c.d * c.es / 16) * kDeep; }
-static int chunk_count(const PagedView &c, int stride) { return (stride + chunk_rows(c) - 1) / chunk_rows(c); }
+// items of a list when a thread carries `deep` rows, and evict_shift's
+static int item_count(const PagedView &c, int stride, int deep) {
+    const int rows = kMoveThreads / (c.d * c.es / 16) * deep;
+    return (stride + rows - 1) / rows;
+}
+static int chunk_count(const PagedView &c, int stride) { return item_count(c, stride, kShiftDeep); }
 
 // chunks that the tickets may have to count
 bool evict_countable(const PagedView &c, int budget) {
@@ -514,13 +523,14 @@ cudaError_t evict_launch(const PagedView &src, const PagedView &dst, bool in_pla
                         ? select_launch<1024>(src, dst, in_place, budget, sink, recent, ranks, slots, stride, list, plan, in_place ? flags : nullptr, chunks, status, s)
                         : select_launch<512>(src, dst, in_place, budget, sink, recent, ranks, slots, stride, list, plan, in_place ? flags : nullptr, chunks, status, s);
     if (e != cudaSuccess) return e;
-    const long long blocks = (long long)kCopyBlocksPerSm * sm_count();
     if (in_place) {
         const long long items = (long long)nh * chunks;
+        const long long blocks = (long long)kShiftBlocksPerSm * sm_count();
         return launch_behind(K_EVICT_MOVE, evict_shift_kernel, (int)(items < blocks ? items : blocks), kMoveThreads, 0, s,
                              src, stride, chunks, list, plan, flags, flags + (size_t)nh * chunks, status);
     }
-    const long long items = (long long)nh * (chunks + 1);
+    const long long items = (long long)nh * (item_count(src, stride, kDeep) + 1);
+    const long long blocks = (long long)kCopyBlocksPerSm * sm_count();
     return launch_behind(K_EVICT_MOVE, evict_copy_kernel, (int)(items < blocks ? items : blocks), kMoveThreads, 0, s, src,
                          dst, stride, list, plan, status);
 }
