@@ -9,6 +9,7 @@
 #include <vector>
 
 #include "common.cuh"
+#include "paged.cuh"
 #include "tc.cuh"
 
 namespace gdn2 {
@@ -70,10 +71,10 @@ struct PendingTiming {
 static std::mutex g_timer_mu;
 static std::atomic<bool> g_timer_on{false};
 static std::vector<PendingTiming> g_pending;
-static cudaEvent_t g_open_start[K_KINDS];
-static unsigned long long g_kind_count[K_KINDS];
-static double g_kind_ms[K_KINDS];
-static const char *const g_kind_names[K_KINDS] = {
+static cudaEvent_t g_open_start[K_ALL_KINDS];
+static unsigned long long g_kind_count[K_ALL_KINDS];
+static double g_kind_ms[K_ALL_KINDS];
+static const char *const g_kind_names[K_ALL_KINDS] = {
     "simt_chunk_prep", "simt_state_fwd", "simt_out_fwd", "simt_state_bwd", "simt_chunk_bwd_a",
     "simt_chunk_bwd_b", "decode_step", "tc_prep", "tc_fwd", "tc_bwd_state", "tc_bwd_grad", "seq_table",
     "permute_state", "seg_link", "kv_append", "kv_lens", "attn_split", "attn_finish", "evict_select",
@@ -591,16 +592,16 @@ void gdn2_set_kernel_timer(int enable) {
         cudaEventDestroy(p.end);
     }
     g_pending.clear();
-    for (int i = 0; i < K_KINDS; ++i) {
+    for (int i = 0; i < K_ALL_KINDS; ++i) {
         g_kind_count[i] = 0;
         g_kind_ms[i] = 0.0;
     }
     g_timer_on.store(enable != 0);
 }
 
-int gdn2_kernel_kinds(void) { return K_KINDS; }
+int gdn2_kernel_kinds(void) { return K_ALL_KINDS; }
 
-const char *gdn2_kernel_name(int id) { return id >= 0 && id < K_KINDS ? g_kind_names[id] : nullptr; }
+const char *gdn2_kernel_name(int id) { return id >= 0 && id < K_ALL_KINDS ? g_kind_names[id] : nullptr; }
 
 gdn2_status gdn2_kernel_times(unsigned long long *count, double *ms, int n) {
     std::lock_guard<std::mutex> lock(g_timer_mu);
@@ -618,7 +619,7 @@ gdn2_status gdn2_kernel_times(unsigned long long *count, double *ms, int n) {
         cudaEventDestroy(p.end);
     }
     g_pending.clear();
-    for (int i = 0; i < n && i < K_KINDS; ++i) {
+    for (int i = 0; i < n && i < K_ALL_KINDS; ++i) {
         if (count) count[i] = g_kind_count[i];
         if (ms) ms[i] = g_kind_ms[i];
     }

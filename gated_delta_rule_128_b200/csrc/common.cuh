@@ -205,13 +205,10 @@ struct SimtWs {
 enum KernelKind {
     K_SIMT_PREP = 0, K_SIMT_STATE_FWD, K_SIMT_OUT, K_SIMT_STATE_BWD, K_SIMT_BWD_A, K_SIMT_BWD_B,
     K_DECODE, K_TC_PREP, K_TC_FWD, K_TC_BWD_STATE, K_TC_BWD_GRAD, K_SEQ_TABLE,
-    K_PERMUTE_STATE, K_SEG_LINK, K_KV_APPEND, K_KV_LENS, K_ATTN_SPLIT, K_ATTN_FINISH,
-    K_EVICT_SELECT, K_EVICT_MOVE, K_KINDS
+    K_PERMUTE_STATE, K_SEG_LINK, K_KINDS
 };
 void launch_begin(int kind, cudaStream_t s);
 void launch_end(int kind, cudaStream_t s);
-// device address of the status word in the current context (nullptr on failure)
-unsigned int *status_word();
 
 inline size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
 

@@ -6,6 +6,13 @@
 
 namespace gdn2 {
 
+// kernel kinds of these calls, behind common.cuh's
+enum PagedKernelKind {
+    K_KV_APPEND = K_KINDS, K_KV_LENS, K_ATTN_SPLIT, K_ATTN_FINISH, K_EVICT_SELECT, K_EVICT_MOVE, K_ALL_KINDS
+};
+// device address of the status word in the current context (nullptr on failure)
+unsigned int *status_word();
+
 constexpr int kMaxHeadGroup = 256;  // most query heads of a key-value head
 
 struct PagedView {

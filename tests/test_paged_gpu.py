@@ -540,6 +540,24 @@ def test_a_decode_loop_of_both_mixers(mode):
     assert gdn.gdn2_get_device_status() == 0
 
 
+def test_launches_are_counted_and_timed():
+    kv, _ = cache([3000, 40], 16, 2, 64, "bf16", 65, room=1)
+    q, _ = query(2, 4, 64, "bf16", 66)
+    kn = torch.randn(2, 2, 64, device="cuda").to(torch.bfloat16)
+    before = gdn.gdn2_kernel_launches()
+    gdn.gdn2_set_kernel_timer(True)
+    try:
+        gdn.kv_append(kv, kn, kn)
+        gdn.attn_decode_step(q, kv, add_weights=True)
+        gdn.kv_evict(kv, 1000)
+        times = gdn.gdn2_kernel_times()
+    finally:
+        gdn.gdn2_set_kernel_timer(False)
+    assert gdn.gdn2_kernel_launches() - before == 5
+    assert set(times) == {"kv_append", "attn_split", "attn_finish", "evict_select", "evict_move"}
+    assert all(n == 1 and ms > 0 for n, ms in times.values())
+
+
 def test_two_streams_at_once():
     """Two caches on two streams, each call with a workspace of its own."""
     a, ca = cache([4000, 1], 16, 2, 128, "bf16", 60)
