@@ -66,7 +66,7 @@ LENS = [0, 1, 15, 16, 17, 31, 63, 64, 65, 127, 128, 129, 200]
 
 @pytest.mark.parametrize("io", ["bf16", "f32"])
 @pytest.mark.parametrize("d", [32, 64, 128])
-@pytest.mark.parametrize("H_kv,G", [(1, 1), (3, 2), (2, 7), (2, 8), (1, 9), (1, 16), (2, 17), (1, 40)])
+@pytest.mark.parametrize("H_kv,G", [(1, 1), (3, 2), (2, 7), (2, 8), (1, 9), (1, 16), (2, 17), (1, 40), (33, 3)])
 def test_attention_heads_and_sizes(io, d, H_kv, G):
     kv, c = cache(LENS, 16, H_kv, d, io, d + G, fill=NAN)
     q, q64 = query(len(LENS), H_kv * G, d, io, 5)
@@ -100,7 +100,7 @@ def test_attention_window(io, window, add):
 @pytest.mark.parametrize("io,N,H_kv,G,d,lens", [
     ("bf16", 1, 1, 4, 128, (9001,)), ("bf16", 1, 2, 8, 64, (20011,)), ("f32", 1, 1, 3, 128, (7003,)),
     ("bf16", 3, 2, 1, 32, (12000, 1, 333)), ("f32", 4, 2, 16, 32, (0, 5000, 0, 2)),
-    ("bf16", 2, 1, 33, 128, (4097, 6000)),
+    ("bf16", 2, 1, 33, 128, (4097, 6000)), ("bf16", 2, 1, 256, 32, (600, 70)), ("f32", 1, 2, 100, 64, (900,)),
 ])
 @pytest.mark.parametrize("add", [False, True])
 def test_attention_long_caches_are_split_and_joined(io, N, H_kv, G, d, lens, add):
@@ -444,6 +444,23 @@ def test_evict_with_a_budget_beyond_the_table():
     assert all(same(h[x], c2[x]) for x in ("k", "v", "w", "lens"))
 
 
+def test_evict_keys_that_one_block_cannot_hold():
+    """Many sequences, so one block each, and two of them longer than its shared memory has keys."""
+    lens = [50000] + [3] * 150 + [45000, 0]
+    kv, _ = cache_on_gpu(lens, 64, 1, 32, 90)
+    kv.weights.copy_(torch.floor(kv.weights * 50))
+    budget = 20000
+    w = kv.weights.cpu().numpy()
+    table = kv.block_table.cpu().numpy()
+    kept = gdn.kv_evict(kv, budget, sink=1, recent=5, want_kept=True).cpu().numpy()
+    assert gdn.gdn2_get_device_status() == 0
+    for n, x in enumerate(lens):
+        j = np.arange(x)
+        ref = np.array(paged.kept(w[table[n, j // 64], 0, j % 64], x, budget, 1, 5))
+        assert np.array_equal(kept[n, 0, :len(ref)], ref) and (kept[n, 0, len(ref):] == -1).all()
+    assert kv.seq_lens.tolist() == [min(x, budget) for x in lens]
+
+
 @pytest.mark.parametrize("into", [False, True])
 def test_evict_bad_pages_and_lengths(into):
     lens = [100, 60, 33, 5]
@@ -538,6 +555,53 @@ def test_a_decode_loop_of_both_mixers(mode):
                 p, s = paged.place(c, n, j)
                 assert np.array_equal(h["k"][p, s], c["k"][p, s]) and np.array_equal(h["v"][p, s], c["v"][p, s])
     assert gdn.gdn2_get_device_status() == 0
+
+
+def test_a_captured_step_with_eviction_repeats_the_eager_one():
+    """Append, attention with weights and an eviction in one graph, against the same calls
+    made one by one on a copy: every tensor equal, bit for bit, at every step."""
+    a, _ = cache([0, 90, 700, 33], 16, 2, 64, "bf16", 67, room=60, fill=0.0)
+    b = gdn.PagedKV(a.k.clone(), a.v.clone(), a.block_table, a.seq_lens.clone(), a.weights.clone())
+    bufs = [torch.zeros(4, h, 64, dtype=torch.bfloat16, device="cuda") for h in (8, 2, 2)]
+
+    def step(kv):
+        gdn.kv_append(kv, bufs[1], bufs[2])
+        o, lse = gdn.attn_decode_step(bufs[0], kv, add_weights=True, want_lse=True)
+        return o, lse, gdn.kv_evict(kv, 96, sink=1, recent=20, want_kept=True)
+
+    saved = [t.clone() for t in (a.k, a.v, a.seq_lens, a.weights)]
+    step(a)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = step(a)
+    for t, x in zip((a.k, a.v, a.seq_lens, a.weights), saved):
+        t.copy_(x)
+    for i in range(25):
+        for t, x in zip(bufs, decode_inputs(4, 8, 2, 64, 68, i)):
+            t.copy_(x)
+        graph.replay()
+        ref = step(b)
+        assert all(torch.equal(x, y) for x, y in zip(out, ref)), i
+        assert all(torch.equal(x, y) for x, y in ((a.k, b.k), (a.v, b.v), (a.seq_lens, b.seq_lens), (a.weights, b.weights))), i
+    assert max(a.seq_lens.tolist()) == 96 and gdn.gdn2_get_device_status() == 0
+
+
+def test_evictions_on_two_streams_at_once():
+    lens = [6000, 5000]
+    caches = [cache_on_gpu(lens, 16, 4, 128, 95 + i)[0] for i in range(2)]
+    dst = [cache_on_gpu([3000, 3000], 16, 4, 128, 97 + i)[0] for i in range(2)]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    want = [gdn.kv_evict(c, 3000, recent=10, dst=x, want_kept=True) for c, x in zip(caches, dst)]
+    torch.cuda.synchronize()
+    got = [gdn.kv_evict(c, 3000, recent=10, want_kept=True, stream=s) for c, s in zip(caches, streams)]
+    torch.cuda.synchronize()
+    j = torch.arange(3000, device="cuda")
+    for c, x, a, b in zip(caches, dst, want, got):
+        assert torch.equal(a, b)
+        for n in range(2):
+            p, p2 = c.block_table[n, j // 16].long(), x.block_table[n, j // 16].long()
+            assert torch.equal(c.k[p, j % 16], x.k[p2, j % 16]) and torch.equal(c.v[p, j % 16], x.v[p2, j % 16])
 
 
 def test_launches_are_counted_and_timed():
