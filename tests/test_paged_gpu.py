@@ -109,6 +109,17 @@ def test_attention_long_caches_are_split_and_joined(io, N, H_kv, G, d, lens, add
     check(kv, c, q, q64, io, d ** -0.5, 0, add)
 
 
+@pytest.mark.parametrize("width", [1, 100])
+@pytest.mark.parametrize("add", [False, True])
+def test_attention_of_empty_sequences_only(width, add):
+    kv, c = cache([0] * 5, 16, 2, 64, "bf16", 24, fill=NAN)
+    kv = gdn.PagedKV(kv.k, kv.v, torch.full((5, width), -1, dtype=torch.int32, device="cuda"), kv.seq_lens, kv.weights)
+    q, _ = query(5, 4, 64, "bf16", 25)
+    o, lse = gdn.attn_decode_step(q, kv, add_weights=add, want_lse=True, o=torch.full_like(q, NAN))
+    assert (o == 0).all() and torch.isneginf(lse).all() and torch.isnan(kv.weights).all()
+    assert gdn.gdn2_get_device_status() == 0
+
+
 @pytest.mark.parametrize("io", ["bf16", "f32"])
 def test_attention_many_sequences(io):
     """More sequences than blocks and than one pass of a block's threads over the lengths."""
