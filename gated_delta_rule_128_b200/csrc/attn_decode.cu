@@ -294,10 +294,13 @@ struct Ring {
         static_assert(kPieces <= 32 && KW * kPieces % 32 == 0, "whole warps of pieces");
         const int piece = lane % kPieces, mine = lane / kPieces;
         const char *k = a.c.k + piece * 16, *v = a.c.v + piece * 16;
+        long long rows[KW * kPieces / 32];  // all fetched before the first is used
+#pragma unroll
+        for (int x = 0; x < KW * kPieces / 32; ++x) rows[x] = __shfl_sync(0xffffffffu, off, x * kRowsAtOnce + mine);
 #pragma unroll
         for (int x = 0; x < KW * kPieces / 32; ++x) {
             const int r = x * kRowsAtOnce + mine;
-            const long long ro = __shfl_sync(0xffffffffu, off, r);
+            const long long ro = rows[x];
             const uint32_t to = s + at(r, piece);
             if (FULL) {
                 cp_async16_full(to, k + ro);
@@ -368,17 +371,21 @@ struct EngineBf16 {
     template <class R>
     __device__ __forceinline__ void step(const AttnArgs &a, const Segment &sg, uint32_t ks, uint32_t vs, uint32_t live,
                                          int lane, float *scores, float *) {
-        float s[NT][4];
+        float s[NT][4], s2[NT][4];  // two sums, to halve the chain of products (16 heads: 65.8 -> 63.6 us)
         const int mi = lane >> 3, lr = lane & 7, g = lane >> 2, t = lane & 3;
 #pragma unroll
-        for (int i = 0; i < NT; ++i) s[i][0] = s[i][1] = s[i][2] = s[i][3] = 0.f;
+        for (int i = 0; i < NT; ++i) s[i][0] = s[i][1] = s[i][2] = s[i][3] = s2[i][0] = s2[i][1] = s2[i][2] = s2[i][3] = 0.f;
 #pragma unroll
         for (int x = 0; x < D / 16; ++x) {
             uint32_t k[4];
             ldmatrix4(ks + R::at((mi & 1) * 8 + lr, 2 * x + (mi >> 1)), k);
 #pragma unroll
-            for (int i = 0; i < NT; ++i) mma16816(s[i], k, qf[i][x][0], qf[i][x][1]);
+            for (int i = 0; i < NT; ++i) mma16816(x & 1 ? s2[i] : s[i], k, qf[i][x][0], qf[i][x][1]);
         }
+#pragma unroll
+        for (int i = 0; i < NT; ++i)
+#pragma unroll
+            for (int y = 0; y < 4; ++y) s[i][y] += s2[i][y];
         const bool on[2] = {(live >> g & 1u) != 0, (live >> (g + 8) & 1u) != 0};
         float mn[NT][2];
         bool raised = false;
@@ -434,8 +441,8 @@ struct EngineBf16 {
             // to 2^-8, they would add as much error to o as its own rounding
             // (2.2e-3 against 1.7e-3 in all); in two parts it is 2^-16.  The
             // second product costs nothing up to 8 heads, where the copies set
-            // the pace, and 5% with 16 (64 sequences of up to 4000 tokens, 4 kv
-            // heads: 62.7 -> 65.8 us).
+            // the pace, and 3 us of 65 with 16 (64 sequences of up to 4000
+            // tokens, 4 kv heads).
             const uint32_t h0 = tc::pack_bf16(s[i][0], s[i][1]), h1 = tc::pack_bf16(s[i][2], s[i][3]);
             p[i][0] = transpose8x8(h0);
             p[i][1] = transpose8x8(h1);
