@@ -73,7 +73,11 @@ gdn2_status check_heads(const PagedView &c, int H) {
     return H / c.Hkv > kMaxHeadGroup || (long long)c.N * H > 0x7fffffffLL / 64 || !attn_countable(c, H) ? GDN2_ERR_UNSUPPORTED : GDN2_OK;
 }
 
-gdn2_status launched(cudaError_t e) { return e == cudaSuccess ? GDN2_OK : GDN2_ERR_CUDA; }
+gdn2_status launched(cudaError_t e) {
+    if (e == cudaSuccess) return GDN2_OK;
+    cudaGetLastError();  // the caller has the status; a later call does not find the error again
+    return GDN2_ERR_CUDA;
+}
 
 }  // namespace
 

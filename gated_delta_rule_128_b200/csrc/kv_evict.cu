@@ -381,10 +381,11 @@ constexpr int kShiftBlocksPerSm = 2;
 // (sequence, head)s.  A block reads its chunk, says so in the chunk's flag, and
 // writes it once every earlier chunk of that (sequence, head) has been read:
 // row i comes from list[i] >= i, so the rows that chunk x overwrites belong to
-// chunks up to x.  No block waits before it has read its own chunk, and it
-// waits for blocks with earlier tickets only, which are at work already, so
-// every wait ends whichever blocks the GPU runs; it gives up all the same
-// after some seconds (GDN2_ERR_TIMEOUT).  Chunks of 128 rows (bf16, d = 128)
+// chunks up to x.  Every wait ends, whichever blocks the GPU runs: a block
+// waits, with its own chunk read, for chunks of earlier tickets only, so the
+// block that holds the earliest ticket not yet read is either reading it or
+// (the next ticket is drawn early) waits for nothing that is not read.  It
+// gives up all the same after some seconds (GDN2_ERR_TIMEOUT).  Chunks of 128 rows (bf16, d = 128)
 // make the agreement cheap: 16 sequences of up to 8K tokens and 16 heads to 2K
 // take 140 us, with 32 rows and twice the blocks 153; the copy above, 113.
 __global__ void __launch_bounds__(kMoveThreads, kShiftBlocksPerSm)

@@ -257,6 +257,8 @@ gdn2_status gdn2_bwd_varlen(const void *q, const void *k, const void *v, const v
  * it leave that page's tokens out; either records GDN2_ERR_INVALID_ARG in the
  * device status word.  No access leaves the pools.  Neither table, nor the
  * weights, may change while a call that reads them runs.
+ * The first of these calls in a context loads their device code: make it
+ * before any stream capture.
  * Sequences may share pages (a common prompt) in every call that only reads
  * them; a page that a call writes must belong to one sequence, once. */
 typedef struct {
