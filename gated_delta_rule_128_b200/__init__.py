@@ -610,6 +610,8 @@ def kv_evict(kv: PagedKV, budget: int, *, sink: int = 0, recent: int = 0, dst: O
         raise ValueError(f"dst is on {dst.device}, the cache on {kv.device}")
     if not (1 <= budget < 2 ** 31 and 0 <= sink <= budget and 0 <= recent <= budget - sink):
         raise ValueError(f"budget must be at least 1 and sink + recent within it, got {budget}, {sink}, {recent}")
+    if want_kept and budget > 2 ** 30:  # refused before 4 bytes a token of it are allocated
+        raise ValueError(f"want_kept needs a budget of at most 2**30, got {budget}")
     with _on_stream(kv, stream):
         kept = torch.empty(s.N, s.H_kv, budget, dtype=torch.int32, device=kv.device) if want_kept else None
         ws = kv._workspace(ws, "gdn2_kv_evict_workspace_bytes", budget)

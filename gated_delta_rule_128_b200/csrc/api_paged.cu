@@ -137,6 +137,8 @@ gdn2_status gdn2_kv_evict(const gdn2_paged_kv *kv, const gdn2_paged_kv *dst, int
     if (!c.w || budget < 1 || sink < 0 || recent < 0 || (long long)sink + recent > budget || !aligned(kept, 4))
         return GDN2_ERR_INVALID_ARG;
     if (!evict_countable(c, budget)) return GDN2_ERR_UNSUPPORTED;
+    // a kept list has `budget` entries, whatever the table reaches; the kernels count them in ints
+    if (kept && budget > 1 << 30) return GDN2_ERR_UNSUPPORTED;
     if (!ws || !aligned(ws, 16) || ws_bytes < evict_ws_bytes(c, budget)) return GDN2_ERR_WORKSPACE;
     unsigned int *status = status_word();
     if (!status) return GDN2_ERR_CUDA;

@@ -332,7 +332,7 @@ size_t gdn2_kv_evict_workspace_bytes(const gdn2_paged_kv *kv, int budget);
  *   budget >= 1; sink, recent >= 0; sink + recent <= budget; N * H_kv *
  *       min(budget, max_pages * page_size) < 2^33.  kv->weight is needed.
  *   kept : int32 [N, H_kv, budget], each new slot's former index (-1 behind the
- *       new length), or NULL. */
+ *       new length), with budget <= 2^30; or NULL. */
 gdn2_status gdn2_kv_evict(const gdn2_paged_kv *kv, const gdn2_paged_kv *dst, int budget, int sink,
                           int recent, int *kept, void *ws, size_t ws_bytes, gdn2_stream_t stream);
 

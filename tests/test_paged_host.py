@@ -113,6 +113,21 @@ def test_evict_refuses(L, kw, status):
     assert evict(L, **kw) == status
 
 
+@pytest.mark.parametrize("dst", [None, desc(seq_lens=FAKE + 64)])
+def test_evict_refuses_a_kept_list_that_the_kernels_cannot_count(L, dst):
+    """A list of kept tokens has `budget` entries.  Counted in steps of up to 16384 threads, a
+    32-bit index would pass 2^31 and come back below the list.  Without a list any budget goes."""
+    for budget in (2 ** 30 + 1, 2 ** 31 - 16384, 2 ** 31 - 1):
+        assert evict(L, dst=dst, budget=budget, kept=FAKE, ws_bytes=0) == 2
+        assert evict(L, dst=dst, budget=budget, ws_bytes=0) == 3      # as far as the workspace check
+    assert evict(L, dst=dst, budget=2 ** 30, kept=FAKE, ws_bytes=0) == 3
+
+
+def test_binding_refuses_a_kept_list_before_it_allocates_one():
+    with pytest.raises(ValueError, match="want_kept"):
+        gdn.kv_evict(cpu_cache(), 2 ** 30 + 1, want_kept=True)
+
+
 def test_strides_along_single_axes_are_not_read(L):
     """An axis of extent 1 may carry any stride (frameworks leave anything there); the call
     then gets as far as its own arguments."""
