@@ -178,6 +178,12 @@ __device__ __forceinline__ void ldmatrix4_trans(uint32_t addr, uint32_t *r) {
 // the two values of a packed pair of bf16
 __device__ __forceinline__ float bf16_low(uint32_t x) { return __uint_as_float(x << 16); }
 __device__ __forceinline__ float bf16_high(uint32_t x) { return __uint_as_float(x & 0xffff0000u); }
+// a pair of bf16 with infinities, and what is no number, brought to the largest finite value
+__device__ __forceinline__ uint32_t bf16_finite(uint32_t x) {
+    uint32_t y;
+    asm("min.xorsign.abs.bf16x2 %0, %1, %2;" : "=r"(y) : "r"(x), "r"(0x7f7f7f7fu));
+    return y;
+}
 // an 8 x 8 block of 16-bit values (thread 4 r + c holds row r, columns 2c, 2c + 1), transposed
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
     uint32_t y;
@@ -474,10 +480,14 @@ struct EngineBf16 {
             uint32_t v[4];
             ldmatrix4_trans(vs + R::at((mi >> 1) * 8 + lr, 2 * x + (mi & 1)), v);
 #pragma unroll
-            for (int i = 0; i < NT; ++i) {
-                mma16816(acc[i][x], v, p[i][0], p[i][1]);
-                mma16816(acc[i][x], v, rest[i][0], rest[i][1]);
-            }
+            for (int i = 0; i < NT; ++i) mma16816(acc[i][x], v, p[i][0], p[i][1]);
+            // An infinite value is in the sum already.  The rest, which may be 0
+            // or negative, meets the largest finite one in its place (16 heads a
+            // group, 64 sequences of up to 4000 tokens: 67.8 us without, 68.7 with).
+#pragma unroll
+            for (int y = 0; y < 4; ++y) v[y] = bf16_finite(v[y]);
+#pragma unroll
+            for (int i = 0; i < NT; ++i) mma16816(acc[i][x], v, rest[i][0], rest[i][1]);
         }
     }
     // this warp's m, l [kRows] and acc [kRows][D] to shared memory

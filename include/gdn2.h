@@ -307,7 +307,12 @@ size_t gdn2_attn_decode_workspace_bytes(const gdn2_paged_kv *kv, int H, int add_
  *   scale : finite.  The cache is only read.
  * bf16: products on the tensor cores, float32 scores and sums; the softmax
  * weights meet v as sums of two bf16 numbers (off by 2^-16 at most).  float32:
- * all of it in float32. */
+ * all of it in float32.
+ *   Infinities and NaN in v reach their channel alone, as the formula has it:
+ * an infinite v_j makes it infinite, both signs or a NaN make it NaN.  (Weights
+ * below 2^-126 of the sequence's largest may count as 0, and 0 times infinity
+ * is NaN.)  The sum over e^(s_j - max) v_j is divided at its end, so the values
+ * of one channel must not add up beyond float32. */
 gdn2_status gdn2_attn_decode_step(const gdn2_paged_kv *kv, const void *q, void *o, float *lse,
                                   int H, float scale, int window, int add_weights, void *ws,
                                   size_t ws_bytes, gdn2_stream_t stream);

@@ -677,3 +677,37 @@ def test_offsets_beyond_32_bits():
     assert torch.equal(gdn.kv_evict(kv, 33, sink=1, recent=4, want_kept=True),
                        gdn.kv_evict(small, 33, sink=1, recent=4, want_kept=True))
     assert torch.equal(gdn.attn_decode_step(q, kv)[0], gdn.attn_decode_step(q, small)[0])
+
+
+# ------------------------------------------------- values that are not numbers
+
+def agree(o, r, bo):
+    """Equal where the reference is infinite or not a number, within bounds elsewhere."""
+    got, fin = o.double().cpu().numpy(), np.isfinite(r)
+    assert np.array_equal(got[~fin], r[~fin], equal_nan=True)
+    assert (np.abs(got[fin] - r[fin]) <= bo[fin]).all()
+
+
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+@pytest.mark.parametrize("d,G", [(32, 1), (64, 5), (128, 8), (128, 9), (128, 16), (64, 20)])
+@pytest.mark.parametrize("last", [70, 2500])
+def test_attention_infinite_values(io, d, G, last):
+    """A value of +-inf makes its channel +-inf, whatever its token's weight (1 in a sequence of
+    one token), both signs or NaN make it NaN; the other channels are not touched.  In one
+    launch, and (2500 tokens) in parts that are joined."""
+    lens = [1, 40, last]
+    kv, c = cache(lens, 16, 2, d, io, 71, fill=NAN)
+    inf, big = float("inf"), float(torch.finfo(DT[io]).max)
+    for n, j, ch, x in ((0, 0, 3, inf), (0, 0, 4, -inf), (0, 0, 5, NAN), (0, 0, 6, big), (0, 0, 7, -big),
+                        (1, 7, 0, inf), (1, 8, 0, inf), (1, 39, 1, -inf), (1, 0, 2, inf), (1, 31, 2, -inf), (1, 5, 9, NAN),
+                        (2, 0, 1, inf), (2, last - 1, 2, -inf), (2, last // 2, 8, inf), (2, 3, 9, inf), (2, last - 3, 9, -inf)):
+        p, s = paged.place(c, n, j)
+        kv.v[p, s, 1, ch], c["v"][p, s, 1, ch] = x, x
+    q, q64 = query(3, 2 * G, d, io, 72)
+    with np.errstate(invalid="ignore"):
+        r, rl, a, smax = paged.attention(c, q64, d ** -0.5)
+    bo, bl, _ = bounds(io, r, rl, a, smax, last, d)
+    o, lse = gdn.attn_decode_step(q, kv, want_lse=True)
+    agree(o, r, bo)
+    assert (np.abs(lse.double().cpu().numpy() - rl) <= bl).all()
+    assert gdn.gdn2_get_device_status() == 0
