@@ -20,13 +20,18 @@
 // does not leaves (m, l, acc) in the workspace; at most the first and the last
 // of a block's segments are such parts.  attn_finish combines them:
 //   m = max m_i,  o = sum e^(m_i - m) acc_i / sum e^(m_i - m) l_i.
-// Exponents are in base 2 throughout (scale carries log2 e).
+// Exponents are in base 2 throughout (scale carries log2 e).  A running maximum
+// stays within +-FLT_MAX, so that no difference of two of them, or of a score
+// and one, is infinity less itself: scores of -inf sum to 0, and one of +inf to
+// +inf, which the log-sum-exp keeps.
 //
 // Within a block each warp owns 16-token (float32, d = 128: 8-token) slices of
 // its own: it copies their k and v rows into its ring of stages in shared
 // memory with 16-byte asynchronous copies and works on them without a
 // block-wide barrier; the four warps' (m, l, acc) meet once a segment.  The
 // copies run ahead across segments, so a merge does not empty the ring.
+
+#include <float.h>
 
 #include "paged.cuh"
 #include "tc.cuh"
@@ -389,7 +394,7 @@ struct EngineBf16 {
                     qf[i][x][y] = row < sg.rows ? *reinterpret_cast<const uint32_t *>(q + row * D + x * 16 + y * 8 + 2 * t) : 0u;
                 acc[i][x][0] = acc[i][x][1] = acc[i][x][2] = acc[i][x][3] = 0.f;
             }
-            m[i][0] = m[i][1] = -INFINITY;
+            m[i][0] = m[i][1] = -FLT_MAX;
             l[i][0] = l[i][1] = 0.f;
         }
     }
@@ -443,8 +448,8 @@ struct EngineBf16 {
             for (int i = 0; i < NT; ++i)
 #pragma unroll
                 for (int y = 0; y < 2; ++y) {
-                    const float f = mn[i][y] == m[i][y] ? 1.f : exp2f(m[i][y] - mn[i][y]);  // -inf less -inf is no number
-                    m[i][y] = mn[i][y];
+                    const float to = fminf(mn[i][y], FLT_MAX), f = exp2f(m[i][y] - to);
+                    m[i][y] = to;
                     l[i][y] *= f;
 #pragma unroll
                     for (int x = 0; x < D / 16; ++x) {
@@ -458,9 +463,8 @@ struct EngineBf16 {
         for (int i = 0; i < NT; ++i) {
 #pragma unroll
             for (int y = 0; y < 2; ++y) {
-                const float ref = m[i][y] == -INFINITY ? 0.f : m[i][y];
-                s[i][y] = exp2f(s[i][y] - ref);
-                s[i][2 + y] = exp2f(s[i][2 + y] - ref);
+                s[i][y] = exp2f(s[i][y] - m[i][y]);
+                s[i][2 + y] = exp2f(s[i][2 + y] - m[i][y]);
                 l[i][y] += s[i][y] + s[i][2 + y];
             }
             // The weights meet v as the sum of two bf16 numbers: rounded once,
@@ -540,7 +544,7 @@ struct EngineF32 {
 #pragma unroll
         for (int g = 0; g < GP; ++g) {
             acc[g][0] = acc[g][1] = acc[g][2] = acc[g][3] = 0.f;
-            m[g] = -INFINITY;
+            m[g] = -FLT_MAX;
         }
 #pragma unroll
         for (float &x : l) x = 0.f;
@@ -602,7 +606,8 @@ struct EngineF32 {
             float f[GP];
 #pragma unroll
             for (int g = 0; g < GP; ++g) {
-                f[g] = mn[g] == m[g] ? 1.f : exp2f(m[g] - mn[g]);
+                mn[g] = fminf(mn[g], FLT_MAX);
+                f[g] = exp2f(m[g] - mn[g]);
                 m[g] = mn[g];
                 acc[g][0] *= f[g]; acc[g][1] *= f[g]; acc[g][2] *= f[g]; acc[g][3] *= f[g];
             }
@@ -620,15 +625,14 @@ struct EngineF32 {
             if constexpr (GP >= 4) {
 #pragma unroll
                 for (int i = 0; i < kOwn; ++i) {
-                    const float mp = of_part(m + 4 * i, part);
-                    const float e = exp2f(of_part(&s[y][4 * i], part) - (mp == -INFINITY ? 0.f : mp));
+                    const float e = exp2f(of_part(&s[y][4 * i], part) - of_part(m + 4 * i, part));
                     l[i] += e;
                     sp[(tok + 8 * y) * GP + 4 * i + part] = e;
                 }
             } else {
 #pragma unroll
                 for (int g = 0; g < GP; ++g) {
-                    const float e = exp2f(s[y][g] - (m[g] == -INFINITY ? 0.f : m[g]));
+                    const float e = exp2f(s[y][g] - m[g]);
                     l[g] += e;
                     if (part == 0) sp[(tok + 8 * y) * GP + g] = e;
                 }
@@ -691,10 +695,8 @@ __device__ __forceinline__ void store4(__nv_bfloat16 *p, float4 v) {
 }
 
 // what a part with maximum and sum (m, l) = y counts for at the joint maximum m
-// (a part of nothing has none; one of not-a-numbers keeps them)
-__device__ __forceinline__ float part_factor(float2 y, float m) {
-    return y.x == -INFINITY ? (y.y == 0.f ? 0.f : 1.f) : exp2f(y.x - m);
-}
+// (0 for a part of nothing; not-a-numbers in its sums stay what they are)
+__device__ __forceinline__ float part_factor(float2 y, float m) { return exp2f(y.x - m); }
 // the row of ml and part where block b's part of a run, in blocks pr.x .. pr.y,
 // has head `row`: the block where the run begins has it second, the others first
 __device__ __forceinline__ size_t part_row(int2 pr, int b, int row) { return (size_t)(2 * b + (b == pr.x)) * kHeadBlock + row; }

@@ -308,6 +308,8 @@ size_t gdn2_attn_decode_workspace_bytes(const gdn2_paged_kv *kv, int H, int add_
  * bf16: products on the tensor cores, float32 scores and sums; the softmax
  * weights meet v as sums of two bf16 numbers (off by 2^-16 at most).  float32:
  * all of it in float32.
+ *   A score of +inf makes lse +inf and o NaN; other tokens' weights then get 0
+ * from that head.  A score of -inf leaves its token out.
  *   Infinities and NaN in v reach their channel alone, as the formula has it:
  * an infinite v_j makes it infinite, both signs or a NaN make it NaN.  (Weights
  * below 2^-126 of the sequence's largest may count as 0, and 0 times infinity

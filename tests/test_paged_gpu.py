@@ -711,3 +711,51 @@ def test_attention_infinite_values(io, d, G, last):
     agree(o, r, bo)
     assert (np.abs(lse.double().cpu().numpy() - rl) <= bl).all()
     assert gdn.gdn2_get_device_status() == 0
+
+
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+@pytest.mark.parametrize("d,G", [(32, 2), (128, 8), (64, 16)])
+@pytest.mark.parametrize("length", [70, 2500])
+def test_attention_scores_of_plus_infinity(io, d, G, length):
+    """Where a score is +inf, log sum e^s is, e^(s - lse) is 0 for every other token and NaN for
+    that one, and so is o.  Heads that give the same keys -inf leave them out, and what a score
+    that is no number makes of its heads stays NaN."""
+    kv, c = cache([length, 5, 40], 16, 2, d, io, 73, fill=NAN)
+    q, q64 = query(3, 2 * G, d, io, 74)
+    q[:, :, 0], q64[:, :, 0] = 1, 1                      # even heads: +inf
+    q[:, 1::2, 0], q64[:, 1::2, 0] = -1, -1              # odd heads: -inf
+    top = [(0, 3), (0, length // 2), (0, length - 1), (1, 4)]
+    for n, j in top:
+        p, s = paged.place(c, n, j)
+        kv.k[p, s, 1, 0], c["k"][p, s, 1, 0] = float("inf"), float("inf")
+    p, s = paged.place(c, 2, 20)
+    kv.k[p, s, 0, 0], c["k"][p, s, 0, 0] = NAN, NAN
+    w0 = c["w"].copy()
+    finite = dict(c, k=np.where(np.isfinite(c["k"]), c["k"], 0.0), w=w0.copy())
+    smax = paged.attention(finite, q64, d ** -0.5)[3]
+    with np.errstate(invalid="ignore"):
+        r, rl, a, _ = paged.attention(c, q64, d ** -0.5, 0, True)
+    hot = np.zeros(rl.shape, dtype=bool)
+    hot[:2, G::2] = True
+    assert np.isnan(rl[hot]).all()                       # the oracle's inf - inf
+    rl[hot] = np.inf
+    bo, bl, bp = bounds(io, r, rl, a, smax, length, d)
+    o, lse = gdn.attn_decode_step(q, kv, add_weights=True, want_lse=True)
+    assert gdn.gdn2_get_device_status() == 0
+    agree(o, r, bo)
+    agree(lse, rl, bl)
+    # weights of the second key-value head: the odd heads' alone, NaN on the +inf tokens
+    got = kv.weights.double().cpu().numpy()
+    odd = dict(finite, k=c["k"], w=w0.copy())
+    q_odd = q64.copy()
+    q_odd[:, G::2] = q_odd[:, G + 1::2]                  # each odd head twice
+    paged.attention(odd, q_odd, d ** -0.5, 0, True)
+    for n, x in ((0, length), (1, 5)):
+        for j in range(x):
+            p, s = paged.place(c, n, j)
+            if (n, j) in top:
+                assert np.isnan(got[p, 1, s])
+            else:
+                add = (odd["w"][p, 1, s] - w0[p, 1, s]) / 2
+                lim = bp[n].max() * add + (G + 2) * 2.0 ** -24 * (w0[p, 1, s] + add) + 1e-30
+                assert abs(got[p, 1, s] - w0[p, 1, s] - add) <= lim
