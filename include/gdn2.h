@@ -296,9 +296,10 @@ size_t gdn2_attn_decode_workspace_bytes(const gdn2_paged_kv *kv, int H, int add_
 /* Softmax attention of one new token a sequence over its cached tokens:
  *   s_j = scale <q, k_j>, j in [max(0, len - window), len) (window = 0: all),
  *   o = sum_j e^(s_j - lse) v_j,   lse = log sum_j e^(s_j).
- * Query head h reads key-value head h / (H / H_kv); H a multiple of H_kv, at
- * most 256 times it, and N * H * max_pages * page_size < 2^36.  The
- * new token attends to itself once it has been appended.
+ * Query head h reads key-value head h / G, G = H / H_kv; H a multiple of H_kv,
+ * G <= 256, N * H < 2^25 and
+ *   N * H_kv * ceil(G / 16) * (ceil(max_pages * page_size / 64) + 2) < 2^30.
+ * The new token attends to itself once it has been appended.
  *   q, o : [N, H, d] contiguous, io type.   lse : float32 [N, H], or NULL.
  *   A sequence without tokens gets o = 0 and lse = -inf.
  *   add_weights : 1 adds sum over the group's heads of e^(s_j - lse) to the

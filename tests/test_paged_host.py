@@ -91,6 +91,34 @@ def test_attention_refuses(L, kw, status):
     assert attn(L, **kw) == status
 
 
+@pytest.mark.parametrize("N,H_kv,G,page_size,max_pages", [
+    (1 << 20, 1, 1, 64, 1021), ((1 << 20) - 1, 1, 1, 64, 1022),      # N * H_kv * (units + 2)
+    (1 << 20, 1, 1, 32, 2042), (1, 1, 1, 1 << 15, 1 << 15),
+    (1 << 16, 2, 32, 64, 4093), (1 << 16, 2, 33, 64, 2728), (64, 1, 256, 64, (1 << 20) - 3),
+    ((1 << 18) - 1, 1, 128, 16, 1), (3, 4, 256, 16, 100),             # N * H
+])
+def test_attention_takes_what_the_header_promises(L, N, H_kv, G, page_size, max_pages):
+    """Sizes at the stated limits are taken (as far as the workspace check), one step beyond is
+    refused, by the call and by the workspace query alike."""
+    def status(n, table):
+        kv = desc(N=n, H_kv=H_kv, page_size=page_size, max_pages=table, stride_head=64, stride_slot=64 * H_kv,
+                  stride_page=64 * H_kv * page_size)
+        size = L.gdn2_attn_decode_workspace_bytes(ctypes.byref(kv), H_kv * G, 0)
+        rc = attn(L, kv, H=H_kv * G, ws_bytes=0)
+        assert (size == 0) == (rc == 2) and rc in (2, 3)
+        return rc
+
+    def fits(n, table):
+        units = -(-table * page_size // 64) + 2
+        return G <= 256 and n * H_kv * G < 1 << 25 and n * H_kv * -(-G // 16) * units < 1 << 30
+
+    for n in (1, N, N + 1, N + 2, 2 * N):
+        for table in (1, max_pages, max_pages + 1, max_pages + 4):
+            if n * H_kv < 1 << 25 and table * page_size <= 1 << 30:
+                assert status(n, table) == (3 if fits(n, table) else 2)
+    assert fits(N, max_pages)
+
+
 @pytest.mark.parametrize("kw,status", [
     (dict(k=None), 1), (dict(v=None), 1), (dict(k=FAKE + 4), 1), (dict(v=FAKE + 4), 1), (dict(lens=None), 1),
     (dict(lens=FAKE + 2), 1), (dict(cu=FAKE + 2), 1), (dict(T=-1), 1), (dict(cu=None, T=3), 1), (dict(cu=None, T=0), 1),
