@@ -96,6 +96,8 @@ def lib() -> ctypes.CDLL:
         L.gdn2_get_device_status.restype = i
         L.gdn2_selftest_timeout.argtypes = [ctypes.c_longlong, vp]
         L.gdn2_selftest_timeout.restype = i
+        L.gdn2_selftest_evict_timeout.argtypes = [vp, i, vp, sz, ctypes.c_longlong, vp]
+        L.gdn2_selftest_evict_timeout.restype = i
         L.gdn2_status_string.argtypes = [i]
         L.gdn2_status_string.restype = ctypes.c_char_p
         L.gdn2_version.argtypes = []
@@ -288,6 +290,11 @@ def gdn2_get_device_status(stream=None) -> int:
 
 def gdn2_selftest_timeout(limit_cycles: int = 2_000_000, stream=None) -> None:
     _check("gdn2_selftest_timeout", lib().gdn2_selftest_timeout(int(limit_cycles), _stream(stream)))
+
+
+def gdn2_selftest_evict_timeout(kv, budget, ws, ws_bytes, limit_cycles: int = 200_000, stream=None) -> None:
+    rc = lib().gdn2_selftest_evict_timeout(kv.ref, budget, _ptr(ws), ws_bytes, int(limit_cycles), _stream(stream))
+    _check("gdn2_selftest_evict_timeout", rc)
 
 
 def gdn2_kernel_launches() -> int:

@@ -145,4 +145,18 @@ gdn2_status gdn2_kv_evict(const gdn2_paged_kv *kv, const gdn2_paged_kv *dst, int
     return launched(evict_launch(c, to, dst == nullptr, budget, sink, recent, kept, ws, status, (cudaStream_t)stream));
 }
 
+gdn2_status gdn2_selftest_evict_timeout(const gdn2_paged_kv *kv, int budget, void *ws, size_t ws_bytes,
+                                        long long limit_cycles, gdn2_stream_t stream) {
+    PagedView c;
+    gdn2_status st = make_view(c, kv);
+    if (st != GDN2_OK) return st;
+    if (!c.w || budget < 1) return GDN2_ERR_INVALID_ARG;
+    if (!evict_countable(c, budget)) return GDN2_ERR_UNSUPPORTED;
+    if (!ws || !aligned(ws, 16) || ws_bytes < evict_ws_bytes(c, budget)) return GDN2_ERR_WORKSPACE;
+    unsigned int *status = status_word();
+    if (!status) return GDN2_ERR_CUDA;
+    const long long limit = limit_cycles < 1000 ? 1000 : (limit_cycles > 4000000LL ? 4000000LL : limit_cycles);
+    return launched(evict_launch(c, c, true, budget, 0, 0, nullptr, ws, status, (cudaStream_t)stream, limit, c.N * c.Hkv));
+}
+
 }  // extern "C"

@@ -28,8 +28,6 @@ constexpr int kMostRanks = 16;     // blocks of a cluster
 constexpr int kMaxKeys = 40960;    // keys of a block's slice in shared memory
 constexpr int kMoveThreads = 256;
 
-constexpr long long kWaitClocks = 4000000000LL;
-
 __device__ __forceinline__ int ld_acquire(const int *p) {
     int x;
     asm volatile("ld.acquire.gpu.global.s32 %0, [%1];" : "=r"(x) : "l"(p) : "memory");
@@ -85,11 +83,11 @@ __device__ __forceinline__ int block_scan(int x, int *warp_tot) {
 
 // Block (n h, rank) of a cluster.  slots: the keys that dynamic shared memory
 // holds; stride: entries of a list; flags: evict_shift's, one a chunk of each
-// list and the ticket behind them, or nullptr.
+// list and the ticket behind them, or nullptr; ticket: the first to be drawn.
 template <int NT>
 __global__ void __launch_bounds__(NT)
 evict_select_kernel(const PagedView c, const PagedView to, int in_place, int budget, int sink, int recent,
-                    int slots, int stride, int *list_all, EvictPlan *plan, int *flags, int chunks, unsigned int *status) {
+                    int slots, int stride, int *list_all, EvictPlan *plan, int *flags, int chunks, int ticket, unsigned int *status) {
     constexpr int kWarps = NT / 32, kOwn = kBins / NT;  // digits of a thread
     extern __shared__ unsigned s_key[];
     __shared__ __align__(16) int hist[kDigits][kBins];
@@ -103,9 +101,9 @@ evict_select_kernel(const PagedView c, const PagedView to, int in_place, int bud
     const int nh = blockIdx.x / ranks, n = nh / c.Hkv, h = nh - n * c.Hkv;
     int *list = list_all + (size_t)nh * stride;
     follow_previous();
-    if (flags) {  // for evict_shift: no chunk read, no ticket taken
+    if (flags) {  // for evict_shift: no chunk read
         for (int j = rank * NT + tid; j < chunks; j += ranks * NT) flags[(size_t)nh * chunks + j] = 0;
-        if (blockIdx.x == 0 && tid == 0) flags[(size_t)c.N * c.Hkv * chunks] = 0;
+        if (blockIdx.x == 0 && tid == 0) flags[(size_t)c.N * c.Hkv * chunks] = ticket;
     }
     const int raw = c.lens[n];
     int len = checked_len(c, n, status);
@@ -385,12 +383,13 @@ constexpr int kShiftBlocksPerSm = 2;
 // waits, with its own chunk read, for chunks of earlier tickets only, so the
 // block that holds the earliest ticket not yet read is either reading it or
 // (the next ticket is drawn early) waits for nothing that is not read.  It
-// gives up all the same after some seconds (GDN2_ERR_TIMEOUT).  Chunks of 128 rows (bf16, d = 128)
+// gives up all the same after `limit` clocks (GDN2_ERR_TIMEOUT), and leaves its
+// chunk's rows where they were, under lengths that are new already.  Chunks of 128 rows (bf16, d = 128)
 // make the agreement cheap: 16 sequences of up to 8K tokens and 16 heads to 2K
 // take 140 us, with 32 rows and twice the blocks 153; the copy above, 113.
 __global__ void __launch_bounds__(kMoveThreads, kShiftBlocksPerSm)
 evict_shift_kernel(const PagedView c, int stride, int chunks, const int *list_all, const EvictPlan *plan, int *flags,
-                   int *ticket, unsigned int *status) {
+                   int *ticket, long long limit, unsigned int *status) {
     __shared__ int s_ticket;
     const int pieces = c.d * c.es / 16, at_once = kMoveThreads / pieces, nhs = c.N * c.Hkv;
     const int piece = threadIdx.x % pieces, r = threadIdx.x / pieces;
@@ -446,7 +445,7 @@ evict_shift_kernel(const PagedView c, int stride, int chunks, const int *list_al
         for (int j = threadIdx.x; j < chunk && ready; j += kMoveThreads) {
             if (ld_acquire(flag + j)) continue;
             const long long t0 = clock64();
-            while (!ld_acquire(flag + j) && ready) ready = clock64() - t0 < kWaitClocks;
+            while (!ld_acquire(flag + j) && ready) ready = clock64() - t0 < limit;
         }
         if (!__syncthreads_and(ready)) {
             if (threadIdx.x == 0) record_status(status, GDN2_ERR_TIMEOUT);
@@ -495,7 +494,7 @@ size_t evict_ws_bytes(const PagedView &c, int budget) {
 template <int NT>
 static cudaError_t select_launch(const PagedView &src, const PagedView &dst, bool in_place, int budget, int sink, int recent,
                                  int ranks, int slots, int stride, int *list, EvictPlan *plan, int *flags, int chunks,
-                                 unsigned int *status, cudaStream_t s) {
+                                 int ticket, unsigned int *status, cudaStream_t s) {
     const auto kernel = evict_select_kernel<NT>;
     cudaError_t e = cudaSuccess;
     if (slots * 4 > 16 << 10)  // with the static arrays above what any kernel may have
@@ -503,11 +502,12 @@ static cudaError_t select_launch(const PagedView &src, const PagedView &dst, boo
     if (e == cudaSuccess && ranks > 8) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
     if (e != cudaSuccess) return e;
     return launch_clusters(K_EVICT_SELECT, kernel, ranks, src.N * src.Hkv * ranks, NT, slots * 4, s, src, dst, (int)in_place,
-                           budget, sink, recent, slots, stride, list, plan, flags, chunks, status);
+                           budget, sink, recent, slots, stride, list, plan, flags, chunks, ticket, status);
 }
 
 cudaError_t evict_launch(const PagedView &src, const PagedView &dst, bool in_place, int budget, int sink,
-                         int recent, int *kept, void *ws, unsigned int *status, cudaStream_t s) {
+                         int recent, int *kept, void *ws, unsigned int *status, cudaStream_t s, long long wait_clocks,
+                         int ticket) {
     const int nh = src.N * src.Hkv;
     EvictPlan *plan = static_cast<EvictPlan *>(ws);
     const int stride = kept ? budget : list_stride(src, budget);  // entries of a list
@@ -521,14 +521,14 @@ cudaError_t evict_launch(const PagedView &src, const PagedView &dst, bool in_pla
     const int slice = (int)(((long long)src.cap + ranks - 1) / ranks), slots = slice < kMaxKeys ? slice : kMaxKeys;
     // one block an SM has 1024 threads; several hide each other's waits with 512
     cudaError_t e = (long long)nh * ranks <= sm_count()
-                        ? select_launch<1024>(src, dst, in_place, budget, sink, recent, ranks, slots, stride, list, plan, in_place ? flags : nullptr, chunks, status, s)
-                        : select_launch<512>(src, dst, in_place, budget, sink, recent, ranks, slots, stride, list, plan, in_place ? flags : nullptr, chunks, status, s);
+                        ? select_launch<1024>(src, dst, in_place, budget, sink, recent, ranks, slots, stride, list, plan, in_place ? flags : nullptr, chunks, ticket, status, s)
+                        : select_launch<512>(src, dst, in_place, budget, sink, recent, ranks, slots, stride, list, plan, in_place ? flags : nullptr, chunks, ticket, status, s);
     if (e != cudaSuccess) return e;
     if (in_place) {
         const long long items = (long long)nh * chunks;
         const long long blocks = (long long)kShiftBlocksPerSm * sm_count();
         return launch_behind(K_EVICT_MOVE, evict_shift_kernel, (int)(items < blocks ? items : blocks), kMoveThreads, 0, s,
-                             src, stride, chunks, list, plan, flags, flags + (size_t)nh * chunks, status);
+                             src, stride, chunks, list, plan, flags, flags + (size_t)nh * chunks, wait_clocks, status);
     }
     const long long items = (long long)nh * (item_count(src, stride, kDeep) + 1);
     const long long blocks = (long long)kCopyBlocksPerSm * sm_count();

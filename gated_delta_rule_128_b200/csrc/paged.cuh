@@ -100,7 +100,11 @@ cudaError_t attn_launch(const PagedView &c, const void *q, void *o, float *lse, 
                         int window, int add_weights, void *ws, unsigned int *status, cudaStream_t s);
 bool evict_countable(const PagedView &c, int budget);
 size_t evict_ws_bytes(const PagedView &c, int budget);
+constexpr long long kEvictWaitClocks = 4000000000LL;  // about two seconds
+// wait_clocks, ticket: the in-place form's longest wait, and the first ticket
+// that it draws (the self-test leaves the chunks of earlier ones unread)
 cudaError_t evict_launch(const PagedView &src, const PagedView &dst, bool in_place, int budget, int sink,
-                         int recent, int *kept, void *ws, unsigned int *status, cudaStream_t s);
+                         int recent, int *kept, void *ws, unsigned int *status, cudaStream_t s,
+                         long long wait_clocks = kEvictWaitClocks, int ticket = 0);
 
 }  // namespace gdn2

@@ -337,6 +337,9 @@ size_t gdn2_kv_evict_workspace_bytes(const gdn2_paged_kv *kv, int budget);
  *       kv is left as it is (for pages that sequences share).  dst->weight must
  *       be given; strides, page_size and max_pages may differ, dst must hold
  *       min(len, budget) tokens a sequence.
+ *   In place, blocks wait for rows that others have yet to read.  If such a wait
+ * gives up (GDN2_ERR_TIMEOUT in the status word) the cache is not usable any
+ * more: its lengths are shortened and only part of its rows have moved.
  *   budget >= 1; sink, recent >= 0; sink + recent <= budget; N * H_kv *
  *       min(budget, max_pages * page_size) < 2^33.  kv->weight is needed.
  *   kept : int32 [N, H_kv, budget], each new slot's former index (-1 behind the
@@ -399,6 +402,16 @@ gdn2_status gdn2_get_device_status(gdn2_stream_t stream);
  * reports the timeout and clears it.  Returns GDN2_ERR_CUDA if the launch
  * fails.  Not tied to any entry in the pages. */
 gdn2_status gdn2_selftest_timeout(long long limit_cycles, gdn2_stream_t stream);
+
+/* The same for the wait of gdn2_kv_evict in place, whose blocks wait for rows
+ * that other blocks have yet to read: an eviction to `budget` in which nobody
+ * takes the first chunk (64 to 512 rows) of any list that moves more.  Blocks that
+ * wait for it give up after about `limit_cycles` SM clocks (clamped to
+ * [1e3, 4e6]) each, record GDN2_ERR_TIMEOUT and leave their rows where they
+ * were; the lengths are shortened all the same.  Arguments and workspace as
+ * for gdn2_kv_evict.  Not tied to any entry in the pages. */
+gdn2_status gdn2_selftest_evict_timeout(const gdn2_paged_kv *kv, int budget, void *ws, size_t ws_bytes,
+                                        long long limit_cycles, gdn2_stream_t stream);
 
 /* Static, never NULL. */
 const char *gdn2_status_string(gdn2_status status);

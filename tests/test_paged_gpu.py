@@ -759,3 +759,26 @@ def test_attention_scores_of_plus_infinity(io, d, G, length):
                 add = (odd["w"][p, 1, s] - w0[p, 1, s]) / 2
                 lim = bp[n].max() * add + (G + 2) * 2.0 ** -24 * (w0[p, 1, s] + add) + 1e-30
                 assert abs(got[p, 1, s] - w0[p, 1, s] - add) <= lim
+
+
+def test_eviction_in_place_gives_up_a_wait_and_says_so():
+    """Nobody reads the first chunk of rows, so whoever would write over it gives up: the status
+    says so, no row has moved (a write before its read would show), and the context is usable."""
+    lens, budget = [3000, 40, 2000], 1200
+    kv, _ = cache_on_gpu(lens, 16, 2, 64, 110)
+    before = [t.clone() for t in (kv.k, kv.v, kv.weights, kv.seq_lens)]
+    ws = torch.empty(kv.workspace_bytes("gdn2_kv_evict_workspace_bytes", budget), dtype=torch.uint8, device="cuda")
+    gdn.gdn2_selftest_evict_timeout(kv, budget, ws, ws.nbytes)
+    assert gdn.gdn2_get_device_status() == 5          # GDN2_ERR_TIMEOUT
+    for t, x in zip((kv.k, kv.v, kv.weights), before):
+        assert torch.equal(t, x)
+    assert kv.seq_lens.tolist() == [1200, 40, 1200]
+    kv.seq_lens.copy_(before[3])
+    dst, _ = cache_on_gpu([min(x, budget) for x in lens], 16, 2, 64, 111)
+    a = gdn.kv_evict(kv, budget, dst=dst, want_kept=True)
+    b = gdn.kv_evict(kv, budget, want_kept=True, ws=ws)
+    assert gdn.gdn2_get_device_status() == 0 and torch.equal(a, b)
+    for n, x in enumerate(lens):
+        j = torch.arange(min(x, budget), device="cuda")
+        p, p2 = kv.block_table[n, j // 16].long(), dst.block_table[n, j // 16].long()
+        assert torch.equal(kv.k[p, j % 16], dst.k[p2, j % 16]) and torch.equal(kv.v[p, j % 16], dst.v[p2, j % 16])

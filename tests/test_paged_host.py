@@ -156,6 +156,16 @@ def test_binding_refuses_a_kept_list_before_it_allocates_one():
         gdn.kv_evict(cpu_cache(), 2 ** 30 + 1, want_kept=True)
 
 
+@pytest.mark.parametrize("kw,status", [
+    (dict(kv=desc(d=48)), 2), (dict(kv=desc(weight=None)), 1), (dict(budget=0), 1), (dict(ws=None), 3),
+    (dict(ws_bytes=16), 3), (dict(kv=desc(N=1 << 20, max_pages=1 << 20), budget=1 << 24), 2),
+])
+def test_the_evictions_selftest_refuses(L, kw, status):
+    a = dict(kv=desc(), budget=8, ws=FAKE, ws_bytes=BIG)
+    a.update(kw)
+    assert L.gdn2_selftest_evict_timeout(ctypes.byref(a["kv"]), a["budget"], a["ws"], a["ws_bytes"], 1000, None) == status
+
+
 def test_strides_along_single_axes_are_not_read(L):
     """An axis of extent 1 may carry any stride (frameworks leave anything there); the call
     then gets as far as its own arguments."""
