@@ -110,6 +110,10 @@ gdn2_status gdn2_attn_decode_step(const gdn2_paged_kv *kv, const void *q, void *
     if (st != GDN2_OK) return st;
     if ((st = check_heads(c, H)) != GDN2_OK) return st;
     if (!q || !o || !aligned(q, 16) || !aligned(o, 16) || !aligned(lse, 4)) return GDN2_ERR_INVALID_ARG;
+    // o in q's place is written after q has been read, unless the weights need q again
+    const size_t bytes = (size_t)c.N * H * c.d * c.es;
+    const uintptr_t qa = (uintptr_t)q, oa = (uintptr_t)o;
+    if (qa < oa + bytes && oa < qa + bytes && (qa != oa || add_weights)) return GDN2_ERR_INVALID_ARG;
     if (window < 0 || !isfinite(scale * 1.5f)  /* with log2 e in it too */ || (add_weights && !c.w)) return GDN2_ERR_INVALID_ARG;
     if (!ws || !aligned(ws, 16) || ws_bytes < attn_ws_bytes(c, H, add_weights != 0)) return GDN2_ERR_WORKSPACE;
     unsigned int *status = status_word();

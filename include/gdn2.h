@@ -300,7 +300,8 @@ size_t gdn2_attn_decode_workspace_bytes(const gdn2_paged_kv *kv, int H, int add_
  * G <= 256, N * H < 2^25 and
  *   N * H_kv * ceil(G / 16) * (ceil(max_pages * page_size / 64) + 2) < 2^30.
  * The new token attends to itself once it has been appended.
- *   q, o : [N, H, d] contiguous, io type.   lse : float32 [N, H], or NULL.
+ *   q, o : [N, H, d] contiguous, io type; o may be q itself unless add_weights
+ *       is set, and must not overlap it otherwise.   lse : float32 [N, H], or NULL.
  *   A sequence without tokens gets o = 0 and lse = -inf.
  *   add_weights : 1 adds sum over the group's heads of e^(s_j - lse) to the
  *       weight of each token read (kv->weight must be given).  Where sequences

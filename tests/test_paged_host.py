@@ -91,6 +91,14 @@ def test_attention_refuses(L, kw, status):
     assert attn(L, **kw) == status
 
 
+def test_attention_refuses_an_output_over_its_queries(L):
+    """The weights of tokens whose scores were not kept need q after o has been written."""
+    size = 2 * 8 * 64 * 2
+    for o, add, status in ((FAKE, 1, 1), (FAKE, 0, 3), (FAKE + 128, 0, 1), (FAKE - 128, 0, 1), (FAKE + size - 16, 1, 1),
+                           (FAKE + 16 - size, 0, 1), (FAKE + size, 1, 3), (FAKE - size, 1, 3)):
+        assert attn(L, o=o, add=add, ws_bytes=0) == status, (o - FAKE, add)
+
+
 @pytest.mark.parametrize("N,H_kv,G,page_size,max_pages", [
     (1 << 20, 1, 1, 64, 1021), ((1 << 20) - 1, 1, 1, 64, 1022),      # N * H_kv * (units + 2)
     (1 << 20, 1, 1, 32, 2042), (1, 1, 1, 1 << 15, 1 << 15),

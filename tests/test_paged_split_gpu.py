@@ -168,3 +168,16 @@ def test_shared_prompts_hold_more_than_the_pool(io, d, G, prompt, N):
         assert (np.abs(got - c["w"])[fin] <= lim[fin]).all()
         assert np.array_equal(np.isnan(got), ~fin)
         c["w"][:] = got
+
+
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+@pytest.mark.parametrize("lens", [[100, 3], [3000, 3, 0, 700]])
+def test_the_output_may_take_the_queries_place(io, lens):
+    kv, _ = cache(lens, 16, 2, 64, io, 112)
+    q, _ = query(len(lens), 2 * 20, 64, io, 113)
+    want, lse = gdn.attn_decode_step(q, kv, want_lse=True)
+    o, lse2 = gdn.attn_decode_step(q, kv, o=q, want_lse=True)
+    assert o is q and torch.equal(o, want) and torch.equal(lse, lse2)
+    with pytest.raises(gdn.Gdn2Error) as e:
+        gdn.attn_decode_step(q, kv, o=q, add_weights=True)
+    assert e.value.status == 1
