@@ -8,7 +8,7 @@ import torch
 import gated_delta_rule_128_b200 as gdn
 from _paged import bounds, cache
 from oracle import paged
-from test_paged_gpu import NAN, _lib, _status, check, query  # noqa: F401  (the fixtures apply here too)
+from test_paged_gpu import NAN, _lib, _status, cache_on_gpu, check, query  # noqa: F401  (the fixtures apply here too)
 
 pytestmark = pytest.mark.gpu
 
@@ -181,3 +181,82 @@ def test_the_output_may_take_the_queries_place(io, lens):
     with pytest.raises(gdn.Gdn2Error) as e:
         gdn.attn_decode_step(q, kv, o=q, add_weights=True)
     assert e.value.status == 1
+
+
+# ------------------------------------------------------------- the longest tables
+
+PAGE = 1 << 20
+
+
+def one_page_many_times(io, seed):
+    """A sequence of 2^30 tokens, the most that a table may reach: one page of 2^20 tokens 1024
+    times over."""
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    k, v = (torch.randn(1, PAGE, 1, 32, device="cuda", generator=g).to({"bf16": torch.bfloat16, "f32": torch.float32}[io])
+            for _ in range(2))
+    v += 1
+    return gdn.PagedKV(k, v, torch.zeros(1, 1024, dtype=torch.int32, device="cuda"),
+                       torch.full((1,), 1 << 30, dtype=torch.int32, device="cuda"),
+                       torch.zeros(1, 1, PAGE, device="cuda")), g
+
+
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+@pytest.mark.parametrize("window", [0, (1 << 30) - 5])
+def test_attention_over_two_to_the_thirty_tokens(io, window):
+    """Every page's tokens again and again: o is that of one page, lse log 1024 more, each weight
+    1024 times the page's."""
+    kv, g = one_page_many_times(io, 114)
+    q = torch.randn(1, 2, 32, device="cuda", generator=g).to(kv.k.dtype)
+    o, lse = gdn.attn_decode_step(q, kv, window=window, add_weights=True, want_lse=True)
+    assert gdn.gdn2_get_device_status() == 0
+    z = q[0].double() @ kv.k[0, :, 0].double().T * 32 ** -0.5
+    p, v = torch.softmax(z, -1), kv.v[0, :, 0].double()
+    ref, spread = p @ v, p @ v.abs()
+    # A lane adds 2^30 / (148 * 4 blocks * 4 warps) tokens in steps of 16 or 8, two sums a step, so
+    # fewer than 2^18 additions in a row, each off by at most 2^-23 (the tensor cores' truncate)
+    # of sums that grow evenly (half of the last on average): 2^-6 of sum p |v| for o's numerator
+    # and of l alike.  A block's tokens left out or read twice would change lse by 1/600.
+    assert ((o[0].double() - ref).abs() <= 2.0 ** -5 * spread + 2.0 ** -8 * ref.abs()).all()
+    assert ((lse[0].double() - torch.logsumexp(z, -1) - np.log(1024)).abs() <= 2.0 ** -6).all()
+    # 1024 additions to each weight, each rounding by 2^-24 of what is there, after lse's error
+    want = p.sum(0)
+    assert ((kv.weights[0, 0].double() - want).abs() <= (2.0 ** -5 + 1024 * 2.0 ** -24) * want).all()
+
+
+def test_eviction_from_two_to_the_thirty_tokens():
+    """The heaviest tokens are the page's heaviest one, 1024 times; equal weights go by index."""
+    kv, g = one_page_many_times("bf16", 115)
+    kv.weights.copy_(torch.randperm(PAGE, device="cuda", generator=g).float())
+    best = int(kv.weights.argmax())
+    k, v = (torch.zeros(11, 100, 1, 32, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    dst = gdn.PagedKV(k, v, torch.arange(11, dtype=torch.int32, device="cuda")[None], torch.zeros(1, dtype=torch.int32, device="cuda"),
+                      torch.zeros(11, 1, 100, device="cuda"))
+    kept = gdn.kv_evict(kv, 1003, sink=1, recent=2, dst=dst, want_kept=True)
+    assert gdn.gdn2_get_device_status() == 0
+    want = [0] + [best + i * PAGE for i in range(1000)] + [(1 << 30) - 2, (1 << 30) - 1]
+    assert best not in (0, PAGE - 1, PAGE - 2) and kept[0, 0].tolist() == want
+    assert dst.seq_lens.tolist() == [1003] and kv.seq_lens.tolist() == [1 << 30]
+    j = torch.arange(1003, device="cuda")
+    src = kept[0, 0].long() % PAGE
+    assert torch.equal(dst.k[j // 100, j % 100, 0], kv.k[0, src, 0]) and torch.equal(dst.v[j // 100, j % 100, 0], kv.v[0, src, 0])
+
+
+@pytest.mark.parametrize("into", [False, True])
+def test_eviction_of_keys_that_a_cluster_cannot_hold(into):
+    """A sequence of a million tokens: 16 blocks share it, and each has more keys than its shared
+    memory takes."""
+    x, budget, P = 1000003, 300000, 64
+    kv, _ = cache_on_gpu([x], P, 1, 32, 116)
+    kv.weights.copy_(torch.floor(kv.weights * 5000))
+    dst = cache_on_gpu([budget], P, 1, 32, 117)[0] if into else None
+    k0, w0, table = kv.k.clone(), kv.weights.clone(), kv.block_table[0].long()
+    kept = gdn.kv_evict(kv, budget, sink=3, recent=100, dst=dst, want_kept=True)[0, 0].long()
+    assert gdn.gdn2_get_device_status() == 0
+    j = torch.arange(x, device="cuda")
+    w = w0[table[j // P], 0, j % P][3:x - 100]
+    best = torch.sort(w, descending=True, stable=True).indices[:budget - 103] + 3
+    assert torch.equal(kept, torch.cat([j[:3], best.sort().values, j[x - 100:]]))
+    to = dst if into else kv
+    i = torch.arange(budget, device="cuda")
+    assert torch.equal(to.k[to.block_table[0].long()[i // P], i % P], k0[table[kept // P], kept % P])
+    assert to.seq_lens.tolist() == [budget]
