@@ -782,3 +782,41 @@ def test_eviction_in_place_gives_up_a_wait_and_says_so():
         j = torch.arange(min(x, budget), device="cuda")
         p, p2 = kv.block_table[n, j // 16].long(), dst.block_table[n, j // 16].long()
         assert torch.equal(kv.k[p, j % 16], dst.k[p2, j % 16]) and torch.equal(kv.v[p, j % 16], dst.v[p2, j % 16])
+
+
+@pytest.mark.parametrize("into", [False, True])
+def test_the_c_calls_under_their_own_names(into):
+    """gdn2_kv_append, gdn2_attn_decode_step and gdn2_kv_evict with the caller's buffers, on a
+    stream of the caller's: what kv_append, attn_decode_step and kv_evict leave, bit for bit."""
+    budget = 64
+    cu = torch.tensor([0, 900, 900, 930], dtype=torch.int32, device="cuda")
+    k, v = (torch.randn(930, 2, 64, device="cuda").to(torch.bfloat16) for _ in range(2))
+    q, _ = query(3, 8, 64, "bf16", 118)
+    a, _ = cache([5, 0, 17], 16, 2, 64, "bf16", 119, room=900, fill=0.0)
+    b = gdn.PagedKV(a.k.clone(), a.v.clone(), a.block_table, a.seq_lens.clone(), a.weights.clone())
+    dst = [cache_on_gpu([budget] * 3, 16, 2, 64, 120)[0] for _ in range(2)] if into else [None, None]
+    gdn.kv_append(a, k, v, cu_seqlens=cu)
+    o, lse = gdn.attn_decode_step(q, a, scale=0.1, window=700, add_weights=True, want_lse=True)
+    kept = gdn.kv_evict(a, budget, sink=2, recent=7, dst=dst[0], want_kept=True)
+    side = torch.cuda.Stream()
+    o2, lse2, kept2 = torch.full_like(o, NAN), torch.full_like(lse, NAN), torch.full_like(kept, -5)
+    n1, n2 = gdn.gdn2_attn_decode_workspace_bytes(b, 8, True), gdn.gdn2_kv_evict_workspace_bytes(b, budget)
+    ws1, ws2 = (torch.empty(n, dtype=torch.uint8, device="cuda") for n in (n1, n2))
+    torch.cuda.synchronize()
+    gdn.gdn2_kv_append(b, k, v, cu, 930, b.seq_lens, stream=side)
+    gdn.gdn2_attn_decode_step(b, q, o2, lse2, 8, 0.1, 700, True, ws1, n1, stream=side)
+    gdn.gdn2_kv_evict(b, dst[1], budget, 2, 7, kept2, ws2, n2, stream=side)
+    assert gdn.gdn2_get_device_status(side) == 0
+    for x, y in ((o, o2), (lse, lse2), (kept, kept2)):
+        assert torch.equal(x, y)
+    for x, y in ((a, b), dst) if into else ((a, b),):
+        assert all(torch.equal(s, t) for s, t in ((x.k, y.k), (x.v, y.v), (x.weights, y.weights), (x.seq_lens, y.seq_lens)))
+    with pytest.raises(gdn.Gdn2Error) as e:
+        gdn.gdn2_attn_decode_step(b, q, o2, lse2, 8, 0.1, 700, True, ws1, n1 - 256)
+    assert e.value.status == 3
+    with pytest.raises(gdn.Gdn2Error) as e:
+        gdn.gdn2_kv_append(b, k, v, None, 930, b.seq_lens)
+    assert e.value.status == 1
+    with pytest.raises(gdn.Gdn2Error) as e:
+        gdn.gdn2_kv_evict(b, None, 0, 0, 0, None, ws2, n2)
+    assert e.value.status == 1
