@@ -12,8 +12,10 @@
 // are on the device, so each block finds its own run with a scan over them).
 // Before each (sequence, head)'s units stand kLead empty ones, for the time
 // that starting and merging it takes: without them a block that gets 28 short
-// sequences needs twice as long as one with 28 units of a long one (64
-// sequences of 1 to 1000 tokens, 16 heads: 85 us without them, 51 with them).
+// sequences needs twice as long as one with 28 units of a long one (48
+// sequences of 1 to 1000 tokens, 16 heads: 60 us without them, 41 with them; 64
+// of 1 to 4000: 195 and 180).  Times in this file are a call's on the GPU, in a
+// captured graph; d = 128, bf16, inputs from HBM, where nothing else is said.
 // A block walks the part of its run that lies in one (sequence, head) as a
 // segment with a running maximum m, sum l and accumulator of e^(s - m) v.  A
 // segment that covers the whole (sequence, head) leaves the result, one that
@@ -42,15 +44,17 @@ constexpr int kAttnWarps = 4;
 constexpr int kAttnThreads = 32 * kAttnWarps;
 constexpr int kUnit = 64;        // tokens of a unit
 constexpr int kLead = 2;         // empty units before a (sequence, head)'s own
-constexpr int kMinUnits = 1;     // fewest units of a block: one sequence of 1000 tokens, 16 heads, takes 8.9 us with 1, 9.6 with 2
+constexpr int kMinUnits = 1;     // fewest units of a block: one sequence of 1000 tokens, 16 heads, takes 9.4 us with 1, 9.8 with 2
 constexpr int kHeadBlock = 16;   // most query heads of one pass
 constexpr int kMostBlocksPerSm = 4;
 // Sequences that cannot hold more than kSoloTokens (or kSoloTokensMany where
 // there are kSoloRuns (sequence, head)s for each block that the GPU holds, so
 // that blocks with short ones make room for others) go to blocks one
-// (sequence, head) each: no search for a run, and no join.  One sequence of
-// 500 tokens, 16 heads: 8.8 us and one launch, split 9.0 and two; of 1000 14.6
-// against 8.9.  1024 (sequence, head)s of up to 2000 tokens: 84 us, split 89.
+// (sequence, head) each: no search for a run, no join, and one launch, which
+// counts where the host takes longer than the GPU (10 us a call from Python).
+// One sequence, 16 heads: 100 tokens 4.8 us, split 8.0; 300 8.0 and 8.3; 400 9.7
+// and 8.6; 500 10.6 and 8.8 (8.2 and 8.3 out of L2); 1000 17 and 9.4.  1024
+// (sequence, head)s of up to 2000 tokens: 91 us, split 95; of up to 1000 48, 53.
 constexpr int kSoloTokens = 512;
 constexpr int kSoloTokensMany = 2048;
 constexpr int kSoloRuns = 3;
@@ -94,7 +98,7 @@ __device__ __forceinline__ Run find_run(const PagedView &c, int window, int per,
     __shared__ int s_warp[NT / 32], s_n, s_base;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     // A warp's lanes cover the sequences: each warp for itself, without barriers
-    // (one sequence of 1000 tokens, 16 heads over 2: 8.6 us with them, 8.2 without).
+    // (one sequence of 1000 tokens, 16 heads over 2: 8.4 us with them, 8.0 without).
     if (c.N <= 32) {
         const int own = lane < c.N ? units_of(c, lane, window, status) : 0;
         int sum = own;
@@ -402,21 +406,17 @@ struct EngineBf16 {
     template <class R>
     __device__ __forceinline__ void step(const AttnArgs &a, const Segment &sg, uint32_t ks, uint32_t vs, uint32_t live,
                                          int lane, float *scores, float *) {
-        float s[NT][4], s2[NT][4];  // two sums, to halve the chain of products (16 heads: 65.8 -> 63.6 us)
+        float s[NT][4];
         const int mi = lane >> 3, lr = lane & 7, g = lane >> 2, t = lane & 3;
 #pragma unroll
-        for (int i = 0; i < NT; ++i) s[i][0] = s[i][1] = s[i][2] = s[i][3] = s2[i][0] = s2[i][1] = s2[i][2] = s2[i][3] = 0.f;
+        for (int i = 0; i < NT; ++i) s[i][0] = s[i][1] = s[i][2] = s[i][3] = 0.f;
 #pragma unroll
         for (int x = 0; x < D / 16; ++x) {
             uint32_t k[4];
             ldmatrix4(ks + R::at((mi & 1) * 8 + lr, 2 * x + (mi >> 1)), k);
 #pragma unroll
-            for (int i = 0; i < NT; ++i) mma16816(x & 1 ? s2[i] : s[i], k, qf[i][x][0], qf[i][x][1]);
+            for (int i = 0; i < NT; ++i) mma16816(s[i], k, qf[i][x][0], qf[i][x][1]);
         }
-#pragma unroll
-        for (int i = 0; i < NT; ++i)
-#pragma unroll
-            for (int y = 0; y < 4; ++y) s[i][y] += s2[i][y];
         const bool on[2] = {(live >> g & 1u) != 0, (live >> (g + 8) & 1u) != 0};
         float mn[NT][2];
         bool raised = false;
@@ -471,7 +471,7 @@ struct EngineBf16 {
             // to 2^-8, they would add as much error to o as its own rounding
             // (2.2e-3 against 1.7e-3 in all); in two parts it is 2^-16.  The
             // second product costs nothing up to 8 heads, where the copies set
-            // the pace, and 3 us of 65 with 16 (64 sequences of up to 4000
+            // the pace, and 3 us of 66 with 16 (64 sequences of up to 4000
             // tokens, 4 kv heads).
             const uint32_t h0 = tc::pack_bf16(s[i][0], s[i][1]), h1 = tc::pack_bf16(s[i][2], s[i][3]);
             p[i][0] = transpose8x8(h0);
@@ -486,8 +486,8 @@ struct EngineBf16 {
 #pragma unroll
             for (int i = 0; i < NT; ++i) mma16816(acc[i][x], v, p[i][0], p[i][1]);
             // An infinite value is in the sum already.  The rest, which may be 0
-            // or negative, meets the largest finite one in its place (16 heads a
-            // group, 64 sequences of up to 4000 tokens: 67.8 us without, 68.7 with).
+            // or negative, meets the largest finite one in its place (1 us of
+            // those 66, nothing up to 8 heads).
 #pragma unroll
             for (int y = 0; y < 4; ++y) v[y] = bf16_finite(v[y]);
 #pragma unroll
