@@ -12,8 +12,8 @@ namespace gdn2 {
 
 constexpr int kAppThreads = 256;
 constexpr int kAppTokens = 64;  // most tokens of one block
-// Bytes of k and v for one block: 17.5K prompt tokens of 16 KB take 47.4 us with
-// 32 KB or 48 KB a block, 50 with 112 KB, 55 with 256 KB, 53 with 16 KB.
+// Bytes of k and v for one block: 17.5K prompt tokens of 16 KB take 48.6 us with
+// 32 KB a block, 47.5 with 16 KB, 49 with 48 KB, 58 with 112 KB, 51 with 256 KB.
 constexpr int kAppBytes = 32 << 10;
 
 // cu[0 .. N] rises from 0 to T; every thread of the block gets the answer

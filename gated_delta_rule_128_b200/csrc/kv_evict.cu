@@ -264,7 +264,7 @@ evict_select_kernel(const PagedView c, const PagedView to, int in_place, int bud
 // of one (sequence, head), a thread carrying the same 16-byte piece of kDeep
 // rows of k and of v; the next item's places are looked up (list, then tables)
 // while this one's rows are on their way.  The weights are items of their own.
-constexpr int kDeep = 2;  // 16 sequences to 2K tokens of 16 heads: 113 us; with 4 rows a thread 121 to 127, with 8 149
+constexpr int kDeep = 2;  // 16 sequences to 2K tokens of 16 heads: 114 us a call; with 4 rows a thread 146, with 8 262
 constexpr int kCopyBlocksPerSm = 4;
 
 // The most rows that any of the lists moves, for every thread of the block:
@@ -386,7 +386,8 @@ constexpr int kShiftBlocksPerSm = 2;
 // gives up all the same after `limit` clocks (GDN2_ERR_TIMEOUT), and leaves its
 // chunk's rows where they were, under lengths that are new already.  Chunks of 128 rows (bf16, d = 128)
 // make the agreement cheap: 16 sequences of up to 8K tokens and 16 heads to 2K
-// take 140 us, with 32 rows and twice the blocks 153; the copy above, 113.
+// take 141 us, with 32 rows and twice the blocks 153; the copy above, 114.  One
+// of 131K tokens, halved: 80, 117 and 47.
 __global__ void __launch_bounds__(kMoveThreads, kShiftBlocksPerSm)
 evict_shift_kernel(const PagedView c, int stride, int chunks, const int *list_all, const EvictPlan *plan, int *flags,
                    int *ticket, long long limit, unsigned int *status) {

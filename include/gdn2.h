@@ -290,7 +290,10 @@ gdn2_status gdn2_kv_append(const gdn2_paged_kv *kv, const void *k, const void *v
 
 /* Bytes of device workspace (at least 256) that gdn2_attn_decode_step needs for
  * H query heads on the current device; 0 where the sizes are unsupported.  256
- * says that the call does not touch it, so that calls at once may share it. */
+ * says that the call does not touch it, so that calls at once may share it.
+ * With add_weights it holds scores, 4 bytes a token and query head, for as many
+ * tokens as the table reaches, or as the pool has and 192 a sequence more if
+ * that is less (tables of up to 2048 tokens a sequence: always as they reach). */
 size_t gdn2_attn_decode_workspace_bytes(const gdn2_paged_kv *kv, int H, int add_weights);
 
 /* Softmax attention of one new token a sequence over its cached tokens:
@@ -325,7 +328,12 @@ gdn2_status gdn2_attn_decode_step(const gdn2_paged_kv *kv, const void *q, void *
  * the sizes are unsupported. */
 size_t gdn2_kv_evict_workspace_bytes(const gdn2_paged_kv *kv, int budget);
 
-/* Brings every sequence of more than `budget` tokens back to `budget`.  Each
+/* Only gdn2_attn_decode_step with add_weights adds to the weights: those of
+ * appended tokens are 0 until a token attends to them, and among equal weights
+ * eviction keeps the earliest tokens.  Right after a long prompt the caller
+ * therefore fills kv->weight for it, or attends with its last queries first.
+ *
+ * Brings every sequence of more than `budget` tokens back to `budget`.  Each
  * key-value head on its own keeps the first `sink` tokens, the last `recent`
  * ones, and of those between the budget - sink - recent with the largest
  * weight (equal weights: the earlier token; NaN counts below everything).
